@@ -160,6 +160,15 @@ void prof_begin(int id, cudaStream_t s);
 void prof_end(int id, cudaStream_t s);
 void count_launch(int n = 1);
 
+// Multiprocessors of the current device.
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 148;
+  return n;
+}
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int dtype_size(int dtype) { return dtype == HSTU_BF16 ? 2 : 4; }
 

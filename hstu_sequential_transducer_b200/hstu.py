@@ -24,9 +24,16 @@ LIB_PATH = os.path.join(_HERE, "libhstu_debug.so" if DEBUG_BUILD else "libhstu.s
 HSTU_F32, HSTU_BF16 = 0, 1
 SAVED_PRE, SAVED_G, SAVED_O, SAVED_Z, SAVED_MEAN, SAVED_RSTD, SAVED_XLOW, SAVED_COUNT = range(8)
 K_PROJ_IN, K_ATTN_FWD, K_LN_FWD, K_PROJ_OUT, K_PROJ_OUT_BWD, K_LN_BWD, K_ATTN_BWD, \
-    K_PROJ_IN_BWD, K_ATTN_CACHED, K_MISC, K_SOFTMAX, K_COUNT = range(12)
+    K_PROJ_IN_BWD, K_ATTN_CACHED, K_MISC, K_SOFTMAX, K_EMBED, K_BLOCK_NORM, K_CHECKPOINT, \
+    K_COUNT = range(15)
 KERNEL_NAMES = ["proj_in", "attn_fwd", "ln_fwd", "proj_out", "proj_out_bwd", "ln_bwd",
-                "attn_bwd", "proj_in_bwd", "attn_cached", "misc", "softmax_fwd"]
+                "attn_bwd", "proj_in_bwd", "attn_cached", "misc", "softmax_fwd", "embed",
+                "block_norm", "checkpoint"]
+NORM_NONE, NORM_LAYER, NORM_RMS = range(3)
+GATE_NONE, GATE_SIGMOID, GATE_SILU = range(3)
+CKPT_INT8, CKPT_E4M3 = range(2)
+CKPT_PRE, CKPT_DEV, CKPT_X, CKPT_PRE_SCALE, CKPT_DEV_SCALE, CKPT_X_SCALE, CKPT_MEAN, CKPT_RSTD, \
+    CKPT_COUNT = range(9)
 
 FLAG_OFFSETS_START, FLAG_OFFSETS_ORDER, FLAG_OFFSETS_END = 0x1, 0x2, 0x4
 FLAG_SEQ_TOO_LONG, FLAG_TARGETS_RANGE, FLAG_TIME_ORDER = 0x8, 0x10, 0x20
@@ -49,6 +56,17 @@ class Grads(Structure):
     _fields_ = [("dW1", c_void_p), ("db1", c_void_p), ("dW2", c_void_p), ("db2", c_void_p),
                 ("dgamma", c_void_p), ("dbeta", c_void_p), ("drab_pos", c_void_p),
                 ("drab_time", c_void_p)]
+
+
+class CBlockNorm(Structure):
+    _fields_ = [("post_kind", c_int32), ("pre_kind", c_int32), ("gate_act", c_int32),
+                ("reserved", c_int32), ("post_gamma", c_void_p), ("post_beta", c_void_p),
+                ("res_scale", c_void_p), ("pre_gamma", c_void_p), ("pre_beta", c_void_p)]
+
+
+class CBlockNormGrads(Structure):
+    _fields_ = [("post_gamma", c_void_p), ("post_beta", c_void_p), ("res_scale", c_void_p),
+                ("pre_gamma", c_void_p), ("pre_beta", c_void_p)]
 
 
 class HSTUError(RuntimeError):
@@ -88,6 +106,19 @@ _SIGS = {
     "hstu_sl_subsequence_length": (I64, [I64, c_double]),
     "hstu_stochastic_length": (I32, [P, P, I32, I64, I64, P, P, P, P, P]),
     "hstu_gather_rows": (I32, [P, I64, I64, P, P, I64, I64, P, I64, P]),
+    "hstu_embedding_fwd": (I32, [P, I32, I64, I32, I64, P, I32, I64, c_float, P, I32, I32, I64, P,
+                                 I64, P]),
+    "hstu_embedding_bwd_workspace_size": (S, [I64, I64, I32]),
+    "hstu_embedding_bwd": (I32, [P, I32, I64, P, I32, I64, I64, I32, c_float, P, I64, P, S, P]),
+    "hstu_embedding_bwd_rows": (I32, [P, I32, I64, P, I32, I64, I64, I32, c_float, P, P, I64, P, P,
+                                      S, P]),
+    "hstu_block_norm_fwd": (I32, [_CP, POINTER(CBlockNorm), P, P, P, I64, I64, P, P, P, P]),
+    "hstu_block_norm_bwd": (I32, [_CP, POINTER(CBlockNorm), P, P, P, I64, P, P, P, I64, P, P, P,
+                                  I64, POINTER(CBlockNormGrads), P, S, P]),
+    "hstu_block_norm_bwd_workspace_size": (S, [_CP, I64]),
+    "hstu_checkpoint_layout": (I32, [_CP, I64, POINTER(c_size_t)]),
+    "hstu_checkpoint_save": (I32, [_CP, I32, P, I64, P, P]),
+    "hstu_checkpoint_restore": (I32, [_CP, I32, P, P, P, I64, P, P]),
     "hstu_profiler_enable": (None, [I32]),
     "hstu_nvtx_enable": (None, [I32]),
     "hstu_profiler_collect": (I32, [I32, POINTER(c_int64), POINTER(c_double)]),
@@ -411,6 +442,285 @@ def gather_rows(src, gather_index, d_num_rows, out, stream=None):
                                   stream_ptr(stream)),
            "hstu_gather_rows")
     return out
+
+
+# ----------------------------------------------------------------------------
+# Shared by the calls below: checks of their tensors, the device they run on
+# ----------------------------------------------------------------------------
+
+_DTYPE_IDS = {torch.float32: HSTU_F32, torch.bfloat16: HSTU_BF16}
+
+
+def _rows(where, name, t, rows, width, dtype, device):
+    """Checks a [rows][width] tensor with unit inner stride; returns its row stride."""
+    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != rows or \
+            t.shape[1] != width or (t.stride(1) != 1 and width > 1):
+        raise ValueError(f"{where}: {name} must be [{rows}][{width}] {dtype} on {device} with unit "
+                         f"inner stride, got {tuple(t.shape)} {t.dtype} on {t.device}, strides "
+                         f"{t.stride()}")
+    return t.stride(0) if rows > 1 else max(t.stride(0), width)
+
+
+def _flat(where, name, t, shape, dtype, device):
+    """Checks a contiguous tensor of this shape (a None is let through)."""
+    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or
+                          not t.is_contiguous()):
+        raise ValueError(f"{where}: {name} must be contiguous {tuple(shape)} {dtype} on {device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _launch(where, device, stream, f, *args, ws_bytes=None):
+    """Calls the entry point f(*args[, workspace, bytes], stream) on the tensors' device.  A
+    workspace comes from the caching allocator on the stream that the kernels run on, so that no
+    two calls, streams or captured graphs share one."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: needs CUDA tensors, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(where, device, stream, f, *args, ws_bytes=ws_bytes)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    if s.device_index != device.index:
+        raise ValueError(f"{where}: the stream belongs to cuda:{s.device_index}, the tensors to {device}")
+    if ws_bytes is None:
+        _check(f(*args, s.cuda_stream), where)
+        return
+    if stream is None:
+        ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=device)
+    _check(f(*args, ws.data_ptr(), ws_bytes, s.cuda_stream), where)
+
+
+# ----------------------------------------------------------------------------
+# Embedding lookup and its gradient
+# ----------------------------------------------------------------------------
+
+def _ids(where, ids, device):
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 1 or ids.device != device or \
+            not ids.is_contiguous():
+        raise ValueError(f"{where}: ids must be contiguous [T] int32 or int64 on {device}, got "
+                         f"{tuple(ids.shape)} {ids.dtype} on {ids.device}")
+    return ids.shape[0], ids.element_size()
+
+
+def embedding_fwd(table, ids, scale: float = 1.0, out=None, low=None, out_dtype=torch.float32,
+                  stream=None):
+    """out[t] = scale * table[ids[t]] (zero where the id is outside the table); returns out.  out
+    [T][width] with width >= the table's (further columns are zeroed), fp32 or bf16; low: an
+    optional bf16 copy of an fp32 out, as fwd's x_low takes it."""
+    where = "embedding_fwd"
+    dev = table.device
+    T, ib = _ids(where, ids, dev)
+    if table.dim() != 2 or table.dtype not in _DTYPE_IDS:
+        raise ValueError(f"{where}: table must be [V][dim] fp32 or bf16")
+    V, dim = table.shape
+    ts = _rows(where, "table", table, V, dim, table.dtype, dev)
+    if out is None:
+        out = torch.empty(T, dim, dtype=out_dtype, device=dev)
+    if out.dtype not in _DTYPE_IDS or out.dim() != 2:
+        raise ValueError(f"{where}: out must be [T][width] fp32 or bf16")
+    width = out.shape[1]
+    os_ = _rows(where, "out", out, T, width, out.dtype, dev)
+    ls = 0 if low is None else _rows(where, "low", low, T, width, torch.bfloat16, dev)
+    _launch(where, dev, stream, lib().hstu_embedding_fwd, table.data_ptr(), _DTYPE_IDS[table.dtype], V,
+            dim, ts, ids.data_ptr(), ib, T, scale, out.data_ptr(), _DTYPE_IDS[out.dtype], width, os_,
+            ptr(low), ls)
+    return out
+
+
+def _embedding_upstream(where, dout, ids, dim):
+    dev = dout.device
+    T, ib = _ids(where, ids, dev)
+    if dout.dtype not in _DTYPE_IDS or dout.dim() != 2 or dout.shape[1] < dim:
+        raise ValueError(f"{where}: dout must be [T][width] fp32 or bf16 with width >= {dim}")
+    return T, ib, _rows(where, "dout", dout, T, dout.shape[1], dout.dtype, dev)
+
+
+def embedding_bwd(dout, ids, dtable, scale: float = 1.0, stream=None):
+    """dtable[v] += scale * the sum of dout's rows whose id is v (fp32 [V][dim]; dout may be
+    wider, its further columns are not read); returns dtable."""
+    where = "embedding_bwd"
+    V, dim = dtable.shape
+    T, ib, ds = _embedding_upstream(where, dout, ids, dim)
+    gs = _rows(where, "dtable", dtable, V, dim, torch.float32, dout.device)
+    L = lib()
+    _launch(where, dout.device, stream, L.hstu_embedding_bwd, dout.data_ptr(), _DTYPE_IDS[dout.dtype],
+            ds, ids.data_ptr(), ib, T, V, dim, scale, dtable.data_ptr(), gs,
+            ws_bytes=L.hstu_embedding_bwd_workspace_size(T, V, dim))
+    return dtable
+
+
+def embedding_bwd_rows(dout, ids, num_items: int, row_ids, rows, count, scale: float = 1.0, stream=None):
+    """The gradient of a table of num_items rows as its non-zero rows: row_ids [min(T, num_items)]
+    int64 (ascending), rows [min(T, num_items)][dim] fp32 (written), count [1] int64, on the device.
+    Entries past count are left as they were."""
+    where = "embedding_bwd_rows"
+    if rows.dim() != 2:
+        raise ValueError(f"{where}: rows must be [min(T, num_items)][dim]")
+    cap, dim = rows.shape
+    T, ib, ds = _embedding_upstream(where, dout, ids, dim)
+    dev = dout.device
+    rs = _rows(where, "rows", rows, min(T, num_items), dim, torch.float32, dev)
+    _flat(where, "row_ids", row_ids, (cap,), torch.int64, dev)
+    _flat(where, "count", count, (1,), torch.int64, dev)
+    L = lib()
+    _launch(where, dev, stream, L.hstu_embedding_bwd_rows, dout.data_ptr(), _DTYPE_IDS[dout.dtype], ds,
+            ids.data_ptr(), ib, T, num_items, dim, scale, row_ids.data_ptr(), rows.data_ptr(), rs,
+            count.data_ptr(), ws_bytes=L.hstu_embedding_bwd_workspace_size(T, num_items, dim))
+    return row_ids, rows, count
+
+
+# ----------------------------------------------------------------------------
+# Norms before and after a block
+# ----------------------------------------------------------------------------
+
+_NORMS = {None: NORM_NONE, "none": NORM_NONE, "layer": NORM_LAYER, "rms": NORM_RMS}
+_GATES = {None: GATE_NONE, "none": GATE_NONE, "sigmoid": GATE_SIGMOID, "silu": GATE_SILU}
+_PARAMS = ("post_gamma", "post_beta", "res_scale", "pre_gamma", "pre_beta")
+
+
+@dataclass
+class BlockNorm:
+    """The joint of two blocks: kinds "layer", "rms" or None, the gate's activation "silu",
+    "sigmoid" or None (the gate as it is), and [d] parameters in the config's dtype."""
+    post: Optional[str] = "layer"
+    pre: Optional[str] = "layer"
+    gate_act: Optional[str] = None
+    post_gamma: Optional[torch.Tensor] = None
+    post_beta: Optional[torch.Tensor] = None
+    res_scale: Optional[torch.Tensor] = None
+    pre_gamma: Optional[torch.Tensor] = None
+    pre_beta: Optional[torch.Tensor] = None
+
+    def c(self, cfg, where, device) -> CBlockNorm:
+        if self.post not in _NORMS or self.pre not in _NORMS or self.gate_act not in _GATES:
+            raise ValueError(f"{where}: unknown norm or gate activation: {self.post}, {self.pre}, "
+                             f"{self.gate_act}")
+        p = [getattr(self, n) for n in _PARAMS]
+        for n, t in zip(_PARAMS, p):
+            _flat(where, n, t, (cfg.d_model,), torch_dtype(cfg.dtype), device)
+        return CBlockNorm(_NORMS[self.post], _NORMS[self.pre], _GATES[self.gate_act], 0, *map(ptr, p))
+
+
+@dataclass
+class BlockNormGrads:
+    """fp32 [d] gradients of a BlockNorm's parameters, accumulated; None: not wanted."""
+    post_gamma: Optional[torch.Tensor] = None
+    post_beta: Optional[torch.Tensor] = None
+    res_scale: Optional[torch.Tensor] = None
+    pre_gamma: Optional[torch.Tensor] = None
+    pre_beta: Optional[torch.Tensor] = None
+
+    @staticmethod
+    def zeros_like(bn: BlockNorm) -> "BlockNormGrads":
+        z = lambda t: None if t is None else torch.zeros(t.shape, dtype=torch.float32, device=t.device)
+        return BlockNormGrads(*(z(getattr(bn, n)) for n in _PARAMS))
+
+    def c(self, cfg, where, device) -> CBlockNormGrads:
+        p = [getattr(self, n) for n in _PARAMS]
+        for n, t in zip(_PARAMS, p):
+            _flat(where, "grads." + n, t, (cfg.d_model,), torch.float32, device)
+        return CBlockNormGrads(*map(ptr, p))
+
+
+def block_norm_fwd(cfg, bn: BlockNorm, x, b=None, gate=None, y=None, h=None, stats=None, want_h=True,
+                   stream=None):
+    """y = x + res_scale * (Norm_post(b) * act(gate)), h = Norm_pre(y); returns (y, h).  Without b
+    (the start of a stack) y is x; with want_h False (its end) h is None.  stats: fp32 [T][4], kept
+    for block_norm_bwd."""
+    where = "block_norm_fwd"
+    dev, d, T = x.device, cfg.d_model, x.shape[0]
+    io, dt = torch_dtype(cfg.io_dtype), torch_dtype(cfg.dtype)
+    if h is None and want_h:
+        h = torch.empty(T, d, dtype=dt, device=dev)
+    if b is None:
+        y, gate = x, None
+    elif y is None:
+        y = torch.empty_like(x)
+    for n, t, ty in (("x", x, io), ("b", b, io), ("y", y, io), ("h", h, dt)):
+        _flat(where, n, t, (T, d), ty, dev)
+    _flat(where, "stats", stats, (T, 4), torch.float32, dev)
+    gs = 0 if gate is None else _rows(where, "gate", gate, T, d, dt, dev)
+    _launch(where, dev, stream, lib().hstu_block_norm_fwd, ctypes.byref(cfg),
+            ctypes.byref(bn.c(cfg, where, dev)), x.data_ptr(), ptr(b), ptr(gate), gs, T, y.data_ptr(),
+            ptr(h), ptr(stats))
+    return y, h
+
+
+def block_norm_bwd(cfg, bn: BlockNorm, y, b, gate, stats, dy=None, dh=None, dx=None, db=None, dgate=None,
+                   grads: Optional[BlockNormGrads] = None, stream=None):
+    """Backward of block_norm_fwd from dy (upstream of y along the residual stream; None: none) and
+    dh (upstream of h; None: none).  Writes dx (may be dy), db and dgate where given, accumulates
+    grads; returns dx."""
+    where = "block_norm_bwd"
+    dev, d, T = stats.device, cfg.d_model, stats.shape[0]
+    io, dt = torch_dtype(cfg.io_dtype), torch_dtype(cfg.dtype)
+    if dh is not None and y is None:
+        raise ValueError(f"{where}: dh needs y")
+    if b is None and (gate is not None or db is not None or dgate is not None):
+        raise ValueError(f"{where}: gate, db and dgate need b")
+    if dgate is not None and gate is None:
+        raise ValueError(f"{where}: dgate needs gate")
+    if dx is None:
+        dx = torch.empty(T, d, dtype=io, device=dev)
+    for n, t, ty in (("y", y, io), ("b", b, io), ("dy", dy, io), ("dh", dh, io), ("dx", dx, io),
+                     ("db", db, dt)):
+        _flat(where, n, t, (T, d), ty, dev)
+    _flat(where, "stats", stats, (T, 4), torch.float32, dev)
+    gs = 0 if gate is None else _rows(where, "gate", gate, T, d, dt, dev)
+    dgs = 0 if dgate is None else _rows(where, "dgate", dgate, T, d, dt, dev)
+    L = lib()
+    g = None if grads is None else ctypes.byref(grads.c(cfg, where, dev))
+    _launch(where, dev, stream, L.hstu_block_norm_bwd, ctypes.byref(cfg),
+            ctypes.byref(bn.c(cfg, where, dev)), ptr(y), ptr(b), ptr(gate), gs, ptr(stats), ptr(dy),
+            ptr(dh), T, ptr(dx), ptr(db), ptr(dgate), dgs, g,
+            ws_bytes=0 if g is None else L.hstu_block_norm_bwd_workspace_size(ctypes.byref(cfg), T))
+    return dx
+
+
+# ----------------------------------------------------------------------------
+# Activation checkpoints in 8 bits
+# ----------------------------------------------------------------------------
+
+def checkpoint_layout(cfg: Config, T: int):
+    """Byte offsets of a checkpoint's parts and, last, its size."""
+    off = (c_size_t * (CKPT_COUNT + 1))()
+    _check(lib().hstu_checkpoint_layout(ctypes.byref(cfg), T, off), "hstu_checkpoint_layout")
+    return list(off)
+
+
+def checkpoint_bytes(cfg: Config, fmt: int, T: int) -> int:
+    """Size of the checkpoint of one layer's saved block (the same for both formats)."""
+    return checkpoint_layout(cfg, T)[CKPT_COUNT]
+
+
+def _checkpoint_blocks(where, cfg, saved, ckpt, T, fmt):
+    dev = saved.device
+    for n, t, need in (("saved", saved, saved_layout(cfg, T)[SAVED_COUNT]),
+                       ("ckpt", ckpt, checkpoint_bytes(cfg, fmt, T))):
+        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous() or t.numel() < need:
+            raise ValueError(f"{where}: {n} must be at least {need} contiguous bytes on {dev}")
+    return dev
+
+
+def checkpoint_save(cfg: Config, fmt: int, saved, T: int, ckpt, stream=None):
+    """Holds a layer's saved block (filled by fwd) in 8 bits (CKPT_INT8 or CKPT_E4M3); returns ckpt."""
+    dev = _checkpoint_blocks("checkpoint_save", cfg, saved, ckpt, T, fmt)
+    _launch("checkpoint_save", dev, stream, lib().hstu_checkpoint_save, ctypes.byref(cfg), fmt, ptr(saved), T,
+            ptr(ckpt))
+    return ckpt
+
+
+def checkpoint_restore(cfg: Config, fmt: int, ckpt, T: int, ln_gamma, ln_beta, saved, stream=None):
+    """A saved block for bwd from a checkpoint and the layer's ln_gamma, ln_beta; returns saved."""
+    where = "checkpoint_restore"
+    dev = _checkpoint_blocks(where, cfg, saved, ckpt, T, fmt)
+    for n, t in (("ln_gamma", ln_gamma), ("ln_beta", ln_beta)):
+        _flat(where, n, t, (cfg.d_model,), torch_dtype(cfg.dtype), dev)
+    _launch(where, dev, stream, lib().hstu_checkpoint_restore, ctypes.byref(cfg), fmt, ptr(ckpt), ptr(ln_gamma),
+            ptr(ln_beta), T, ptr(saved))
+    return saved
 
 
 # ----------------------------------------------------------------------------

@@ -413,6 +413,174 @@ hstu_status hstu_gather_rows(const void* src, int64_t src_stride_bytes, int64_t 
                              int64_t dst_stride_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Embedding lookup with scaling, and its gradient by sorted ids              */
+/* ------------------------------------------------------------------------ */
+/* The rows x [T][d] of a stack are its events' item embeddings.  With E
+ * [V][dim] the table and id_t the item of event t:
+ *     out[t][c]  = scale * E[id_t][c]   (c < dim),  0  (dim <= c < width)
+ *     dE[v][c]  += scale * sum over t with id_t = v of dout[t][c]
+ * An id outside [0, V) is padding: its row is zero and it has no gradient.
+ *
+ * Common to the entry points below: T < 2^31 rows, 1 <= V < 2^31, 1 <= dim <=
+ * width <= 65,536; ids are int32 or int64 (id_bytes 4 or 8), naturally
+ * aligned; strides are in elements, at least the row's width; rows need only
+ * their element's alignment (wider vectors are used where pointers, strides
+ * and widths allow).  Offsets into the table and the gradient are 64-bit.
+ * No buffer may overlap another. */
+
+/* table [V] rows of dim elements of table_dtype, table_stride apart; out [T]
+ * rows of width elements of out_dtype.  out_low: NULL, or [T] rows of width
+ * bf16 elements receiving the same fp32 products rounded to bf16 (the operand
+ * copy x_low of hstu_fwd_chain); only with out_dtype HSTU_F32. */
+hstu_status hstu_embedding_fwd(const void* table, int32_t table_dtype, int64_t V, int32_t dim,
+                               int64_t table_stride, const void* ids, int32_t id_bytes, int64_t T,
+                               float scale, void* out, int32_t out_dtype, int32_t width,
+                               int64_t out_stride, void* out_low, int64_t low_stride,
+                               cudaStream_t stream);
+
+/* Workspace bytes of the two gradient entry points; 0 for arguments that they
+ * refuse.  Host only. */
+size_t hstu_embedding_bwd_workspace_size(int64_t T, int64_t V, int32_t dim);
+
+/* Dense gradient, fp32, accumulated (+=) into dtable [V] rows of dim.  dout
+ * [T] rows (only its first dim columns are read) of dout_dtype.  Rows of
+ * items that no event names are not touched.  The sums run in the order of
+ * the events in fixed groups, so the result does not change between runs. */
+hstu_status hstu_embedding_bwd(const void* dout, int32_t dout_dtype, int64_t dout_stride,
+                               const void* ids, int32_t id_bytes, int64_t T, int64_t V,
+                               int32_t dim, float scale, float* dtable, int64_t dtable_stride,
+                               void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* The same gradient as rows, for catalogues too large for a dense one:
+ * row_ids[r] (ascending) and rows[r] (fp32, written, not accumulated) for the
+ * *d_num_rows different items that the ids name.  row_ids and rows hold
+ * min(T, V) entries; those from *d_num_rows on are left as they were.  T = 0
+ * writes *d_num_rows = 0. */
+hstu_status hstu_embedding_bwd_rows(const void* dout, int32_t dout_dtype, int64_t dout_stride,
+                                    const void* ids, int32_t id_bytes, int64_t T, int64_t V,
+                                    int32_t dim, float scale, int64_t* row_ids, float* rows,
+                                    int64_t rows_stride, int64_t* d_num_rows, void* workspace,
+                                    size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms before and after a block, with its gate and residual scale           */
+/* ------------------------------------------------------------------------ */
+/* The joint between two blocks of a stack in one pass over the rows: the norm
+ * after a block, its gate and residual scale, the residual sum, and the norm
+ * before the next block.  For a token's row (x the residual stream, b the
+ * block's output, u the gate; (.) elementwise):
+ *     y = x + s (.) (Norm_post(b) (.) act(u))
+ *     h = Norm_pre(y)
+ * Norm(a) = (a - m) r (.) gamma + beta, r = 1/sqrt(mean((a - m)^2) + ln_eps),
+ * m = mean(a) (HSTU_NORM_LAYER) or 0 (HSTU_NORM_RMS); HSTU_NORM_NONE: Norm(a)
+ * = a, without gamma and beta.  h is the norm of y as it is stored.
+ *
+ * x, b, y, dy, dh, dx [T][d] are in cfg->io_dtype and h, u, db, du [T][d] in
+ * cfg->dtype, as the layer's steps take and give them: h is the operand of
+ * hstu_proj_in_fwd, b what hstu_proj_out_fwd writes without a residual, dh
+ * what hstu_proj_in_bwd writes and db the dY of hstu_proj_out_bwd.  u and du
+ * may be columns of wider rows (gate_stride, dgate_stride in elements, at
+ * least d and a multiple of 16 bytes); all else is contiguous.  stats fp32
+ * [T][4] holds each row's m and r after the block, then before the next one.
+ * Without a block (b NULL) y = x, is not written, and u, s and Norm_post do
+ * not apply. */
+typedef enum { HSTU_NORM_NONE = 0, HSTU_NORM_LAYER = 1, HSTU_NORM_RMS = 2 } hstu_norm_kind;
+typedef enum { HSTU_GATE_NONE = 0, HSTU_GATE_SIGMOID = 1, HSTU_GATE_SILU = 2 } hstu_gate_act;
+
+typedef struct {
+  int32_t post_kind;        /* hstu_norm_kind of Norm_post                     */
+  int32_t pre_kind;         /* hstu_norm_kind of Norm_pre                      */
+  int32_t gate_act;         /* act; HSTU_GATE_NONE: act(u) = u                 */
+  int32_t reserved;         /* 0                                               */
+  const void* post_gamma;   /* [d] cfg->dtype each; NULL means 1 (gamma, s)    */
+  const void* post_beta;    /* or 0 (beta)                                     */
+  const void* res_scale;    /* s                                               */
+  const void* pre_gamma;
+  const void* pre_beta;
+} hstu_block_norm;
+
+/* Gradients of the members above, fp32 [d], accumulated (+=); NULL is skipped,
+ * and so are those of a norm that is not there (HSTU_NORM_NONE). */
+typedef struct {
+  float* post_gamma;
+  float* post_beta;
+  float* res_scale;
+  float* pre_gamma;
+  float* pre_beta;
+} hstu_block_norm_grads;
+
+/* b, gate (no gate), y (only without b), h (no Norm_pre: the end of a stack)
+ * and stats may be NULL.  y may be x. */
+hstu_status hstu_block_norm_fwd(const hstu_config* cfg, const hstu_block_norm* bn, const void* x,
+                                const void* b, const void* gate, int64_t gate_stride, int64_t T,
+                                void* y, void* h, float* stats, cudaStream_t stream);
+
+/* From y (x without a block), b, u and stats of the forward, and the upstream
+ * gradients dy (of y along the residual stream; NULL: none) and dh (NULL: h
+ * was not used):
+ *     e  = dy + dNorm_pre(dh)                              -> dx (may be dy)
+ *     db = dNorm_post(e (.) s (.) act(u)),  du = e (.) s (.) Norm_post(b) (.) act'(u)
+ * y may be NULL when dh is.  db, dgate and dx may be NULL: not wanted.  The
+ * parameters' gradients are summed in a fixed order: the result does not
+ * change between runs.  workspace: hstu_block_norm_bwd_workspace_size bytes
+ * (0 when grads is NULL or all its members are). */
+hstu_status hstu_block_norm_bwd(const hstu_config* cfg, const hstu_block_norm* bn, const void* y,
+                                const void* b, const void* gate, int64_t gate_stride,
+                                const float* stats, const void* dy, const void* dh, int64_t T,
+                                void* dx, void* db, void* dgate, int64_t dgate_stride,
+                                const hstu_block_norm_grads* grads, void* workspace,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* Host only; 0 for a cfg that the entry points refuse. */
+size_t hstu_block_norm_bwd_workspace_size(const hstu_config* cfg, int64_t T);
+
+/* ------------------------------------------------------------------------ */
+/* Activation checkpoints in 8 bits                                           */
+/* ------------------------------------------------------------------------ */
+/* A layer's saved block (hstu_saved_layout; 24d + 8 bytes a token with bf16
+ * operands and an fp32 residual stream) in 8 bits, for the time between its
+ * forward and its backward: Pre, the deviations O - mean, X (only where the
+ * block holds it) and each row's mean and rstd; 6.19d + 8 bytes a token.
+ * hstu_checkpoint_restore gives a saved block back for hstu_bwd: Pre, mean
+ * and X as they are held, G = SiLU(Pre), O = mean + deviation and
+ * Z = (deviation * rstd * gamma + beta) (.) U.
+ *
+ * Every 32 values of a row share a power of two 2^k, the smallest with
+ * max |v| <= top * 2^k and k >= -126 (top 127 for HSTU_CKPT_INT8, 448 for
+ * HSTU_CKPT_E4M3; k is at most 121 and 119, and the magnitudes above top * 2^k
+ * that fp32 still has are held as that), and each is held as v * 2^-k rounded to the nearest (ties
+ * to even) whole number, or e4m3 value.  Both steps are exact but for that
+ * one rounding: at most half of 2^k a value (int8), or 2^-4 of it (e4m3, and
+ * 2^-10 of 2^k below 2^(k-6)).  A group with an infinity or NaN is restored
+ * as 32 NaN. */
+typedef enum { HSTU_CKPT_INT8 = 0, HSTU_CKPT_E4M3 = 1 } hstu_ckpt_format;
+
+/* Parts of a checkpoint: the 8-bit values [T][4d], [T][d] and [T][d] of Pre,
+ * O - mean and X, the scales of each as k + 127 in a byte (255: NaN) [T][w/32],
+ * then mean and rstd fp32 [T]. */
+typedef enum {
+  HSTU_CKPT_PRE = 0, HSTU_CKPT_DEV = 1, HSTU_CKPT_X = 2, HSTU_CKPT_PRE_SCALE = 3,
+  HSTU_CKPT_DEV_SCALE = 4, HSTU_CKPT_X_SCALE = 5, HSTU_CKPT_MEAN = 6, HSTU_CKPT_RSTD = 7,
+  HSTU_CKPT_COUNT = 8
+} hstu_ckpt_part;
+
+/* Byte offsets of each hstu_ckpt_part (offsets[HSTU_CKPT_COUNT] = total
+ * bytes), the same for both formats.  Host only. */
+hstu_status hstu_checkpoint_layout(const hstu_config* cfg, int64_t T,
+                                   size_t offsets[HSTU_CKPT_COUNT + 1]);
+
+/* saved: what hstu_fwd filled; ckpt: the total bytes of the layout.  The two
+ * must not overlap. */
+hstu_status hstu_checkpoint_save(const hstu_config* cfg, int32_t format, const void* saved,
+                                 int64_t T, void* ckpt, cudaStream_t stream);
+
+/* ln_gamma, ln_beta: the layer's (hstu_weights), which Z needs; either may be
+ * NULL.  Writes every part of saved. */
+hstu_status hstu_checkpoint_restore(const hstu_config* cfg, int32_t format, const void* ckpt,
+                                    const void* ln_gamma, const void* ln_beta, int64_t T,
+                                    void* saved, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Support                                                                    */
 /* ------------------------------------------------------------------------ */
 
@@ -435,15 +603,16 @@ hstu_status hstu_validate_inputs(const int64_t* seq_offsets, int32_t B, int64_t 
 typedef enum {
   HSTU_K_PROJ_IN = 0, HSTU_K_ATTN_FWD = 1, HSTU_K_LN_FWD = 2, HSTU_K_PROJ_OUT = 3,
   HSTU_K_PROJ_OUT_BWD = 4, HSTU_K_LN_BWD = 5, HSTU_K_ATTN_BWD = 6, HSTU_K_PROJ_IN_BWD = 7,
-  HSTU_K_ATTN_CACHED = 8, HSTU_K_MISC = 9, HSTU_K_SOFTMAX = 10, HSTU_K_COUNT = 11
+  HSTU_K_ATTN_CACHED = 8, HSTU_K_MISC = 9, HSTU_K_SOFTMAX = 10, HSTU_K_EMBED = 11,
+  HSTU_K_BLOCK_NORM = 12, HSTU_K_CHECKPOINT = 13, HSTU_K_COUNT = 14
 } hstu_kernel_id;
 
 void hstu_profiler_enable(int32_t on);
 /* NVTX ranges: while on, each of those regions is also an NVTX push/pop
  * range on the calling host thread, named after its kernel class
  * ("proj_in", "attn_fwd", "ln_fwd", "proj_out", "proj_out_bwd", "ln_bwd",
- * "attn_bwd", "proj_in_bwd", "attn_cached", "misc", "softmax_fwd"), so that an
- * NVTX-aware tracer or `ncu --nvtx` can select the library's steps.  Off by
+ * "attn_bwd", "proj_in_bwd", "attn_cached", "misc", "softmax_fwd", "embed",
+ * "block_norm", "checkpoint"), so that an NVTX-aware tracer or `ncu --nvtx` can select the library's steps.  Off by
  * default; the environment variable HSTU_NVTX=1 turns it on when the library
  * loads.  A switch flipped between a region's begin and end leaves that one
  * range unbalanced: flip it between calls. */
