@@ -10,11 +10,21 @@
 //
 // Memory-bound: the save reads 14d bytes a token and writes 6.19d (bf16
 // operands, fp32 residual stream), the restore reads 6.19d and writes 24d; the
-// arithmetic is a few instructions a value.
+// arithmetic is some 12 instructions a value, most of them on pairs.  So the kernels are
+// plain streams: many small CTAs, each in one part of the block; a thread
+// loads its pieces of 16 bytes (of the wider side) before it works on the first,
+// and neighbouring threads hold neighbouring pieces, so that every access covers
+// whole 32-byte sectors.
+//
+// Measured at 131,072 x 1,024, int8, bf16 operands, fp32 residual stream: save 412 us
+// (6.6 TB/s; 435 with 2 pieces in flight, 555 with 1), restore 647 us
+// (6.3 TB/s; 708 with 4 pieces of V, Q, K and X, 1,216 with 8: the stores of
+// few CTAs come in bursts).
 #include <cuda_fp8.h>
 
 #include "args.h"
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace hstu {
@@ -30,182 +40,366 @@ template <int FMT> constexpr int kScaleMax = FMT == HSTU_CKPT_INT8 ? 121 + 127 :
 // 2^k for k in [-126, 127].
 __device__ __forceinline__ float pow2f(int k) { return __int_as_float((k + 127) << 23); }
 
-// The biased exponent k + 127 of the group whose largest magnitude has these bits.
+// The biased exponent k + 127 of the group whose largest magnitude has these
+// bits: the exponent, one more for a fraction above 127/64 = 1.984375 or 448/256
+// = 1.75 (0x7e0000 and 0x600000 as fractions of 2^23, which the addend carries over).
 template <int FMT>
 __device__ __forceinline__ int scale_of(uint32_t abs_bits) {
-  if (abs_bits >= 0x7f800000u) return kScaleNaN;
-  const int E = (int)(abs_bits >> 23);                       // biased; 0 below 2^-126
-  const uint32_t f = abs_bits & 0x7fffffu;
-  // 127/64 = 1.984375 and 448/256 = 1.75 as fractions of 2^23
-  const int k = FMT == HSTU_CKPT_INT8 ? E - 6 + (f > 0x7e0000u) : E - 8 + (f > 0x600000u);
-  return min(max(k, 1), kScaleMax<FMT>);
+  const int k = FMT == HSTU_CKPT_INT8 ? (int)((abs_bits + 0x1ffffu) >> 23) - 6 : (int)((abs_bits + 0x1fffffu) >> 23) - 8;
+  return abs_bits >= 0x7f800000u ? kScaleNaN : min(max(k, 1), kScaleMax<FMT>);
 }
 
-// Eight values of a group with this scale in 8 bits (e4m3's conversion saturates by itself).
-template <int FMT>
-__device__ __forceinline__ uint2 pack8(float (&f)[8], int scale) {
-  uint32_t w[2];
-  const float inv = pow2f(scale == kScaleNaN ? 0 : 127 - scale);
-  if (FMT == HSTU_CKPT_INT8) {
-    if (scale == kScaleMax<FMT>) {
-      const float top = 127.f * pow2f(kScaleMax<FMT> - 127);
+// 2^k of a held scale; NaN for a group that holds none.
+__device__ __forceinline__ float scale_value(int scale) {
+  return scale == kScaleNaN ? __int_as_float(0x7fffffff) : pow2f(scale - 127);
+}
+
+// W elements of a 16-byte or 8-byte piece, as pairs.
+template <typename T, int W> struct Piece {
+  static constexpr int kWords = W * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kWords == 4) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+  }
+  __device__ __forceinline__ void get(F2 (&f)[W / 2]) const {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -top), top);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // |f inv| <= 127: adding 1.5 2^23 rounds to the nearest whole number
-      // (ties to even) and leaves it in the low byte
-      uint32_t b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(fmaf(f[4 * i + j], inv, 12582912.f));
-      w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      w[i] = lo | (hi << 16);
+    for (int i = 0; i < W / 2; ++i) {
+      if constexpr (sizeof(T) == 4) f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
-  return make_uint2(w[0], w[1]);
-}
-
-template <int FMT>
-__device__ __forceinline__ void unpack8(uint2 q, int scale, float (&f)[8]) {
-  const float s = scale == kScaleNaN ? __int_as_float(0x7fffffff) : pow2f(scale - 127);
-  const uint32_t w[2] = {q.x, q.y};
+  __device__ __forceinline__ void set(const F2 (&f)[W / 2]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (FMT == HSTU_CKPT_INT8) {
-      const uint32_t u = w[i] ^ 0x80808080u;                 // value + 128 in each byte
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        f[4 * i + j] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + j)) - 8388736.f) * s;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> (16 * j)), __NV_E4M3);
-        const float2 t = __half22float2(__half2(h));
-        f[4 * i + 2 * j] = t.x * s;
-        f[4 * i + 2 * j + 1] = t.y * s;
+    for (int i = 0; i < W / 2; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[2 * i] = __float_as_uint(f[i].x);
+        w[2 * i + 1] = __float_as_uint(f[i].y);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].x, f[i].y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
   }
+  // The largest magnitude's bits as fp32 (above infinity's for a NaN).
+  __device__ __forceinline__ uint32_t largest() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = w[0] & 0x7fffffffu;
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    } else {
+      uint32_t m = w[0] & 0x7fff7fffu;               // two at a time
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+      return max(m << 16, m & 0xffff0000u);
+    }
+  }
+};
+// Elements of a 16-byte piece.
+template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
+
+// Two pairs of a group with this scale in 8 bits (e4m3's conversion saturates by itself).
+template <int FMT> __device__ __forceinline__ uint32_t pack4(F2 a, F2 b, F2 inv) {
+  if (FMT == HSTU_CKPT_INT8) {
+    // |a inv| <= 127: adding 1.5 2^23 rounds to the nearest whole number
+    // (ties to even) and leaves it in the low byte
+    const F2 x = fma(a, inv, both(12582912.f)), y = fma(b, inv, both(12582912.f));
+    return __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                       __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
+  }
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul(a, inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul(b, inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
+
+template <int FMT> __device__ __forceinline__ void unpack4(uint32_t w, F2 s, F2& a, F2& b) {
+  if (FMT == HSTU_CKPT_INT8) {
+    const uint32_t u = w ^ 0x80808080u;                 // value + 128 in each byte
+    uint32_t f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __byte_perm(u, 0x4b000000u, 0x7440 + j);    // 2^23 + value + 128
+    a = mul(add(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])), both(-8388736.f)), s);
+    b = mul(add(make_float2(__uint_as_float(f[2]), __uint_as_float(f[3])), both(-8388736.f)), s);
+  } else {
+    a = mul(__half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3))), s);
+    b = mul(__half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3))), s);
+  }
+}
+
+// W packed 8-bit values.
+template <int W> struct Held {
+  uint32_t w[W / 4];
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void store(unsigned char* p) const {
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+  template <int FMT> __device__ __forceinline__ void get(int scale, F2 (&f)[W / 2]) const {
+    const F2 s = both(scale_value(scale));
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) unpack4<FMT>(w[i], s, f[2 * i], f[2 * i + 1]);
+  }
+};
 
 struct CkptPtrs {
   unsigned char *pre, *dev, *x, *pre_s, *dev_s, *x_s;
   float *mean, *rstd;
 };
 
-// One thread for 8 values; units [0, 4n) are Pre's, [4n, 5n) O's, [5n, 6n) X's,
-// n = T d / 8.  n is a multiple of 4 (d is one of 32), so a group's four
-// lanes are in one part; whole warps run every step (the grid is padded).
-template <typename T, int FMT, bool HAS_X>
-__global__ void __launch_bounds__(256) ckpt_save_kernel(const T* __restrict__ pre, const float* __restrict__ o,
-                                                        const T* __restrict__ x, const float* __restrict__ mean,
-                                                        const float* __restrict__ rstd, int64_t rows, int d,
-                                                        CkptPtrs c) {
-  const int64_t n = rows * (d / 8), total = n * (HAS_X ? 6 : 5);
-  const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = i0; i < rows; i += step) {
-    c.mean[i] = mean[i];
-    c.rstd[i] = rstd[i];
+constexpr int kThreads = 256;
+constexpr int kSaveUnroll = 4;       // pieces that a thread has in flight
+
+// The elements of a CTA: [base, base + count) of a part, count at most kThreads
+// W U and a multiple of 32; piece i of a thread begins at its element place(i).
+template <int W> __device__ __forceinline__ int place(int i) { return W * ((int)threadIdx.x + i * kThreads); }
+__device__ __forceinline__ int count_of(int64_t n, int64_t base, int per) { return (int)min((int64_t)per, n - base); }
+
+// Holds a piece at q and its group's scale in scales.  The 32 / W neighbouring
+// lanes of a group have elements (`any`), or none of them has; whole warps take part.
+template <int FMT, typename T, int W>
+__device__ __forceinline__ void hold(F2 (&f)[W / 2], uint32_t largest, bool any, unsigned char* q,
+                                     unsigned char* scales, int at) {
+#pragma unroll
+  for (int o = 16 / W; o > 0; o >>= 1) largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+  if (!any) return;
+  const int k = scale_of<FMT>(largest);
+  if (FMT == HSTU_CKPT_INT8 && k == kScaleMax<FMT>) {
+    const float top = 127.f * pow2f(kScaleMax<FMT> - 127);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+      f[i] = make_float2(fminf(fmaxf(f[i].x, -top), top), fminf(fmaxf(f[i].y, -top), top));
   }
-  const int64_t padded = (total + 31) / 32 * 32;
-  for (int64_t i = i0; i < padded; i += step) {
-    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    unsigned char *q = c.pre, *s = c.pre_s;
-    int64_t u = i;
-    if (i < 4 * n) {
-      load8(pre + u * 8, f);
-    } else if (i < 5 * n) {
-      u = i - 4 * n;
-      q = c.dev;
-      s = c.dev_s;
-      load8(o + u * 8, f);
-      const float mu = mean[u / (d / 8)];
+  const F2 inv = both(pow2f(k == kScaleNaN ? 0 : 127 - k));
+  Held<W> h;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] -= mu;
-    } else if (HAS_X && i < total) {
-      u = i - 5 * n;
-      q = c.x;
-      s = c.x_s;
-      load8(x + u * 8, f);
-    }
-    uint32_t m = 0;
+  for (int i = 0; i < W / 4; ++i) h.w[i] = pack4<FMT>(f[2 * i], f[2 * i + 1], inv);
+  h.store(q + at);
+  if ((threadIdx.x & (kGroup / W - 1)) == 0) scales[at / kGroup] = (unsigned char)k;
+}
+
+// CTA `tile` of an array of n elements.
+template <typename T, int FMT>
+__device__ __forceinline__ void save_tile(const T* src, int64_t n, int64_t tile, unsigned char* q,
+                                          unsigned char* scales) {
+  constexpr int W = kPiece<T>, U = kSaveUnroll, kPer = kThreads * W * U;
+  const int64_t base = tile * kPer;
+  const int count = count_of(n, base, kPer);
+  src += base;
+  Piece<T, W> in[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (i < total) {
-      const int k = scale_of<FMT>(m);
-      if ((u & 3) == 0) s[u >> 2] = (unsigned char)k;
-      *reinterpret_cast<uint2*>(q + u * 8) = pack8<FMT>(f, k);
-    }
+  for (int i = 0; i < U; ++i) {
+    in[i] = {};
+    if (place<W>(i) < count) in[i].load(src + place<W>(i));
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    F2 f[W / 2];
+    in[i].get(f);
+    hold<FMT, T, W>(f, in[i].largest(), place<W>(i) < count, q + base, scales + base / kGroup, place<W>(i));
   }
 }
 
-__device__ __forceinline__ float silu_of(float x) { return x / (1.f + __expf(-x)); }
+// The row of the element `off` (below 2^20) places after the CTA's first: the
+// quotient is at least 1/2d from a whole number, which the fp32 product with
+// 1/d misses by less.
+struct RowOf {
+  int64_t row0;       // row of the CTA's first element
+  int col0;           // and its column
+  float inv;
+  __device__ __forceinline__ RowOf(int64_t e, int d) : row0(e / d), col0((int)(e - row0 * d)), inv(1.f / (float)d) {}
+  __device__ __forceinline__ int rows_after(int off) const { return (int)(((float)(col0 + off) + 0.5f) * inv); }
+};
 
-// One thread for 8 columns of a row: U, V, Q, K, the deviation and X.
-template <typename T, int FMT, bool HAS_X>
-__global__ void __launch_bounds__(256) ckpt_restore_kernel(CkptPtrs c, const T* __restrict__ gamma,
-                                                           const T* __restrict__ beta, int64_t rows, int d,
-                                                           T* __restrict__ pre, T* __restrict__ g,
-                                                           float* __restrict__ o, T* __restrict__ z,
-                                                           T* __restrict__ x, float* __restrict__ mean,
-                                                           float* __restrict__ rstd) {
-  const int units = d / 8;
-  const int64_t total = rows * units;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-    const int64_t r = i / units;
-    const int u = (int)(i - r * units);
-    const float mu = c.mean[r], rs = c.rstd[r];
-    if (u == 0) {
-      mean[r] = mu;
-      rstd[r] = rs;
+// CTAs [0, tp) hold Pre, [tp, tp + td) the deviations, the others X.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const T* __restrict__ pre, const float* __restrict__ o,
+                                                             const T* __restrict__ x, const float* __restrict__ mean,
+                                                             const float* __restrict__ rstd, int64_t rows, int d,
+                                                             int64_t tp, int64_t td, CkptPtrs c) {
+  const int64_t tile = blockIdx.x, n = rows * d;
+  if (tile < tp) {
+    save_tile<T, FMT>(pre, 4 * n, tile, c.pre, c.pre_s);
+    return;
+  }
+  if (tile >= tp + td) {
+    save_tile<T, FMT>(x, n, tile - tp - td, c.x, c.x_s);
+    return;
+  }
+  constexpr int W = kPiece<float>, U = kSaveUnroll, kPer = kThreads * W * U;
+  const int64_t base = (tile - tp) * kPer;
+  const int count = count_of(n, base, kPer);
+  const RowOf where(base, d);
+  o += base;
+  mean += where.row0;
+  rstd += where.row0;
+  Piece<float, W> in[U];
+  float mu[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    in[i] = {};
+    mu[i] = 0.f;
+    if (place<W>(i) < count) {
+      const int r = where.rows_after(place<W>(i));
+      in[i].load(o + place<W>(i));
+      mu[i] = mean[r];
+      if (where.col0 + place<W>(i) == r * d) {       // the row's first piece
+        c.mean[where.row0 + r] = mu[i];
+        c.rstd[where.row0 + r] = rstd[r];
+      }
     }
-    float gate[8];
+  }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int64_t at = r * 4 * units + p * units + u;
-      float f[8], a[8];
-      unpack8<FMT>(*reinterpret_cast<const uint2*>(c.pre + at * 8), c.pre_s[at >> 2], f);
+  for (int i = 0; i < U; ++i) {
+    F2 f[W / 2];
+    in[i].get(f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] = silu_of(f[k]);
-      store8(pre + at * 8, f);
-      store8(g + at * 8, a);
-      if (p == 0)
+    for (int k = 0; k < W / 2; ++k) f[k] = add(f[k], both(-mu[i]));
+    Piece<float, W> p;
+    p.set(f);
+    hold<FMT, float, W>(f, p.largest(), place<W>(i) < count, c.dev + base, c.dev_s + base / kGroup, place<W>(i));
+  }
+}
+
+constexpr int kGateUnroll = 2, kRestUnroll = 2;
+
+// Stores a piece of Pre and its SiLU; leaves that, as it is stored, in f.
+template <typename T, int W>
+__device__ __forceinline__ void store_pre_g(F2 (&f)[W / 2], T* pre, T* g) {
+  Piece<T, W> p;
+  p.set(f);
+  p.store(pre);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) gate[k] = to_f(from_f<T>(a[k]));
+  for (int k = 0; k < W / 2; ++k) f[k] = mul(f[k], sigmoid2(f[k]));
+  p.set(f);
+  p.store(g);
+  p.get(f);
+}
+
+// CTAs [0, tg) restore U with G, O and Z (d columns a row), [tg, tg + tr) V, Q
+// and K with G (3d columns a row), the others X.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(CkptPtrs c, const T* __restrict__ gamma,
+                                                                const T* __restrict__ beta, int64_t rows, int d,
+                                                                int64_t tg, int64_t tr, T* __restrict__ pre,
+                                                                T* __restrict__ g, float* __restrict__ o,
+                                                                T* __restrict__ z, T* __restrict__ x,
+                                                                float* __restrict__ mean, float* __restrict__ rstd) {
+  const int64_t tile = blockIdx.x;
+  if (tile < tg) {
+    constexpr int W = kPiece<float>, U = kGateUnroll, kPer = kThreads * W * U;
+    const int64_t base = tile * kPer;
+    const int count = count_of(rows * d, base, kPer);
+    const RowOf where(base, d);
+    // element e of U is element e + 3d times its row of Pre
+    const int64_t pbase = base + 3 * d * where.row0;
+    int row[U];
+    Held<W> qu[U], qd[U];
+    int su[U], sd[U];
+    float mu[U], rs[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (place<W>(i) >= count) continue;
+      row[i] = where.rows_after(place<W>(i));
+      const int at = place<W>(i) + 3 * d * row[i];
+      qu[i].load(c.pre + pbase + at);
+      qd[i].load(c.dev + base + place<W>(i));
+      su[i] = c.pre_s[(pbase + at) / kGroup];
+      sd[i] = c.dev_s[base / kGroup + place<W>(i) / kGroup];
+      mu[i] = c.mean[where.row0 + row[i]];
+      rs[i] = c.rstd[where.row0 + row[i]];
     }
-    float dv[8], out[8];
-    unpack8<FMT>(*reinterpret_cast<const uint2*>(c.dev + i * 8), c.dev_s[i >> 2], dv);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) out[k] = mu + dv[k];
-    store8(o + i * 8, out);
-    float gm[8], bt[8];
+    for (int i = 0; i < U; ++i) {
+      if (place<W>(i) >= count) continue;
+      const int at = place<W>(i) + 3 * d * row[i], col = where.col0 + place<W>(i) - d * row[i];
+      F2 f[W / 2], dv[W / 2], out[W / 2];
+      qu[i].template get<FMT>(su[i], f);
+      qd[i].template get<FMT>(sd[i], dv);
+      store_pre_g<T, W>(f, pre + pbase + at, g + pbase + at);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      gm[k] = 1.f;
-      bt[k] = 0.f;
+      for (int k = 0; k < W / 2; ++k) out[k] = add(both(mu[i]), dv[k]);
+      Piece<float, W> po;
+      po.set(out);
+      po.store(o + base + place<W>(i));
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) out[k] = mul(dv[k], both(rs[i]));
+      Piece<T, W> p;
+      if (gamma) {
+        F2 t[W / 2];
+        p.load(gamma + col);
+        p.get(t);
+#pragma unroll
+        for (int k = 0; k < W / 2; ++k) out[k] = mul(out[k], t[k]);
+      }
+      if (beta) {
+        F2 t[W / 2];
+        p.load(beta + col);
+        p.get(t);
+#pragma unroll
+        for (int k = 0; k < W / 2; ++k) out[k] = add(out[k], t[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) out[k] = mul(out[k], f[k]);
+      p.set(out);
+      p.store(z + base + place<W>(i));
+      if (col == 0) {
+        mean[where.row0 + row[i]] = mu[i];
+        rstd[where.row0 + row[i]] = rs[i];
+      }
     }
-    if (gamma) load8(gamma + u * 8, gm);
-    if (beta) load8(beta + u * 8, bt);
+    return;
+  }
+  constexpr int W = kPiece<T>, U = kRestUnroll, kPer = kThreads * W * U;
+  if (tile < tg + tr) {
+    const int64_t base = (tile - tg) * kPer;
+    const int count = count_of(3 * rows * d, base, kPer);
+    const RowOf where(base, 3 * d);
+    // element e of V|Q|K is element e + d (its row + 1) of Pre
+    const int64_t pbase = base + d * (where.row0 + 1);
+    int at[U], s[U];
+    Held<W> q[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) out[k] = (dv[k] * rs * gm[k] + bt[k]) * gate[k];
-    store8(z + i * 8, out);
-    if (HAS_X) {
-      unpack8<FMT>(*reinterpret_cast<const uint2*>(c.x + i * 8), c.x_s[i >> 2], out);
-      store8(x + i * 8, out);
+    for (int i = 0; i < U; ++i) {
+      if (place<W>(i) >= count) continue;
+      at[i] = place<W>(i) + d * where.rows_after(place<W>(i));
+      q[i].load(c.pre + pbase + at[i]);
+      s[i] = c.pre_s[(pbase + at[i]) / kGroup];
     }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (place<W>(i) >= count) continue;
+      F2 f[W / 2];
+      q[i].template get<FMT>(s[i], f);
+      store_pre_g<T, W>(f, pre + pbase + at[i], g + pbase + at[i]);
+    }
+    return;
+  }
+  const int64_t base = (tile - tg - tr) * kPer;
+  const int count = count_of(rows * d, base, kPer);
+  Held<W> q[U];
+  int s[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (place<W>(i) >= count) continue;
+    q[i].load(c.x + base + place<W>(i));
+    s[i] = c.x_s[base / kGroup + place<W>(i) / kGroup];
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (place<W>(i) >= count) continue;
+    F2 f[W / 2];
+    q[i].template get<FMT>(s[i], f);
+    Piece<T, W> p;
+    p.set(f);
+    p.store(x + base + place<W>(i));
   }
 }
 
@@ -238,34 +432,43 @@ CkptPtrs ckpt_ptrs(const hstu_config* c, int64_t T, const void* ckpt) {
   return p;
 }
 
-unsigned grid_of(int64_t threads) {
-  const int64_t g = (threads + 255) / 256, cap = (int64_t)sm_count() * 32;
-  return (unsigned)(g > cap ? cap : g);
+// Tiles of `unroll` pieces of W elements a thread in n elements.
+int64_t tiles_of(int64_t n, int W, int unroll) {
+  const int64_t per = (int64_t)kThreads * W * unroll;
+  return (n + per - 1) / per;
 }
 
-template <typename T, int FMT, bool HAS_X>
+template <typename T, int FMT>
 cudaError_t launch_save(const hstu_config* c, const void* saved, int64_t rows, void* ckpt, cudaStream_t s) {
   size_t off[HSTU_SAVED_COUNT + 1];
   saved_offsets(c, rows, off);
   auto* b = static_cast<const unsigned char*>(saved);
-  ckpt_save_kernel<T, FMT, HAS_X><<<grid_of(rows * (c->d_model / 8) * (HAS_X ? 6 : 5)), 256, 0, s>>>(
+  const int64_t n = rows * c->d_model;
+  const int64_t tp = tiles_of(4 * n, kPiece<T>, kSaveUnroll), td = tiles_of(n, kPiece<float>, kSaveUnroll);
+  const int64_t tx = c->io_dtype != c->dtype ? tiles_of(n, kPiece<T>, kSaveUnroll) : 0;
+  if (tp + td + tx > INT32_MAX) return cudaErrorInvalidValue;
+  ckpt_save_kernel<T, FMT><<<(unsigned)(tp + td + tx), kThreads, 0, s>>>(
       reinterpret_cast<const T*>(b + off[HSTU_SAVED_PRE]),
       reinterpret_cast<const float*>(b + off[HSTU_SAVED_O]),
       reinterpret_cast<const T*>(b + off[HSTU_SAVED_XLOW]),
       reinterpret_cast<const float*>(b + off[HSTU_SAVED_MEAN]),
-      reinterpret_cast<const float*>(b + off[HSTU_SAVED_RSTD]), rows, c->d_model, ckpt_ptrs(c, rows, ckpt));
+      reinterpret_cast<const float*>(b + off[HSTU_SAVED_RSTD]), rows, c->d_model, tp, td, ckpt_ptrs(c, rows, ckpt));
   count_launch();
   return cudaGetLastError();
 }
 
-template <typename T, int FMT, bool HAS_X>
+template <typename T, int FMT>
 cudaError_t launch_restore(const hstu_config* c, const void* ckpt, const void* gamma, const void* beta,
                            int64_t rows, void* saved, cudaStream_t s) {
   size_t off[HSTU_SAVED_COUNT + 1];
   saved_offsets(c, rows, off);
   auto* b = static_cast<unsigned char*>(saved);
-  ckpt_restore_kernel<T, FMT, HAS_X><<<grid_of(rows * (c->d_model / 8)), 256, 0, s>>>(
-      ckpt_ptrs(c, rows, ckpt), static_cast<const T*>(gamma), static_cast<const T*>(beta), rows, c->d_model,
+  const int64_t n = rows * c->d_model;
+  const int64_t tg = tiles_of(n, kPiece<float>, kGateUnroll), tr = tiles_of(3 * n, kPiece<T>, kRestUnroll);
+  const int64_t tx = c->io_dtype != c->dtype ? tiles_of(n, kPiece<T>, kRestUnroll) : 0;
+  if (tg + tr + tx > INT32_MAX) return cudaErrorInvalidValue;
+  ckpt_restore_kernel<T, FMT><<<(unsigned)(tg + tr + tx), kThreads, 0, s>>>(
+      ckpt_ptrs(c, rows, ckpt), static_cast<const T*>(gamma), static_cast<const T*>(beta), rows, c->d_model, tg, tr,
       reinterpret_cast<T*>(b + off[HSTU_SAVED_PRE]), reinterpret_cast<T*>(b + off[HSTU_SAVED_G]),
       reinterpret_cast<float*>(b + off[HSTU_SAVED_O]), reinterpret_cast<T*>(b + off[HSTU_SAVED_Z]),
       reinterpret_cast<T*>(b + off[HSTU_SAVED_XLOW]), reinterpret_cast<float*>(b + off[HSTU_SAVED_MEAN]),
@@ -283,11 +486,8 @@ hstu_status check_format(int32_t f) {
 
 using namespace hstu;
 
-// The kernel for the config's types: bf16 with its own copy of X, bf16, fp32.
-#define HSTU_CKPT_DISPATCH(FN, FMT, ...)                                     \
-  (cfg->dtype == HSTU_F32 ? FN<float, FMT, false>(__VA_ARGS__)               \
-   : cfg->io_dtype == HSTU_F32 ? FN<bf16, FMT, true>(__VA_ARGS__)            \
-                               : FN<bf16, FMT, false>(__VA_ARGS__))
+#define HSTU_CKPT_DISPATCH(FN, FMT, ...) \
+  (cfg->dtype == HSTU_F32 ? FN<float, FMT>(__VA_ARGS__) : FN<bf16, FMT>(__VA_ARGS__))
 
 extern "C" {
 
