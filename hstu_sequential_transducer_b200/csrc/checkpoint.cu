@@ -207,17 +207,6 @@ __device__ __forceinline__ void save_tile(const T* src, int64_t n, int64_t tile,
   }
 }
 
-// The row of the element `off` (below 2^20) places after the CTA's first: the
-// quotient is at least 1/2d from a whole number, which the fp32 product with
-// 1/d misses by less.
-struct RowOf {
-  int64_t row0;       // row of the CTA's first element
-  int col0;           // and its column
-  float inv;
-  __device__ __forceinline__ RowOf(int64_t e, int d) : row0(e / d), col0((int)(e - row0 * d)), inv(1.f / (float)d) {}
-  __device__ __forceinline__ int rows_after(int off) const { return (int)(((float)(col0 + off) + 0.5f) * inv); }
-};
-
 // CTAs [0, tp) hold Pre, [tp, tp + td) the deviations, the others X.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const T* __restrict__ pre, const float* __restrict__ o,

@@ -91,6 +91,20 @@ __device__ __forceinline__ void store8(bf16* p, const float (&f)[8]) {
 }
 
 // ---------------------------------------------------------------------------
+// Rows of a CTA's consecutive elements
+// ---------------------------------------------------------------------------
+// The row of the element `off` places after the CTA's first, for rows of d
+// elements with off + d < 2^21: the quotient is at least 1/2d from a whole number,
+// which the fp32 product with 1/d misses by less.
+struct RowOf {
+  int64_t row0;       // row of the CTA's first element
+  int col0;           // and its column
+  float inv;
+  __device__ __forceinline__ RowOf(int64_t e, int d) : row0(e / d), col0((int)(e - row0 * d)), inv(1.f / (float)d) {}
+  __device__ __forceinline__ int rows_after(int off) const { return (int)(((float)(col0 + off) + 0.5f) * inv); }
+};
+
+// ---------------------------------------------------------------------------
 // Small reductions
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float warp_sum(float v) {

@@ -7,16 +7,18 @@
 // and writes T rows (twice with the bf16 copy), the gradient reads T rows and
 // writes one for each different id.
 //
-// Gradient: (id, event) pairs are sorted by id with a stable radix sort of 8
-// bits a pass (as many passes as V has digits; ids outside [0, V) become V and
-// end up last), so that an item's events are neighbours in their own order.
+// Gradient: (id, event) pairs are sorted by id with a stable radix sort of up
+// to 9 bits a pass (as many passes as V has digits; ids outside [0, V) become V
+// and end up last), so that an item's events are neighbours in their own order.
 // A warp then sums a chunk of 32 sorted events: its lanes hold the chunk's
-// (id, event) pairs, every row is read once, and each item's sum leaves the
-// registers when the id changes.  An item whose events lie in one chunk is
-// added to the gradient there; one that crosses into the next chunk leaves a
-// partial sum per chunk, and the chunk where it begins adds those up, so no
-// item's sum depends on the order of execution and a popular item is read by
-// as many warps as it has chunks.
+// (id, event) pairs, every row is read once, 8 of them in flight, and each
+// item's sum leaves the registers when the id changes.  An item whose events lie in
+// one chunk is added to the gradient there; one that crosses into the next chunk
+// leaves a partial sum per chunk, and the chunk where it begins is put on a list
+// whose entries are joined by a last kernel.  No item's sum depends on the
+// order of execution, and a popular item is read by as many warps as it has chunks.
+#include <algorithm>
+
 #include "args.h"
 #include "common.cuh"
 #include "internal.h"
@@ -25,11 +27,20 @@ namespace hstu {
 namespace {
 
 constexpr int kChunk = 32;           // sorted events of a warp
-constexpr int kTile = 2048;          // events of a sorting CTA
-constexpr int kSortThreads = 256;
+constexpr int kBatch = 8;            // rows of a chunk in flight
+constexpr int kSuper = 1024;         // sorted events of a CTA that counts items
+constexpr int kTile = 4096;          // events of a sorting CTA
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kPerThread = kTile / kSortThreads;
-constexpr int kDigits = 256;
+constexpr int kDigits = 512;         // of a pass, at most
+constexpr int kMaxPasses = 4;
+constexpr int kAlone = 32;           // an item that goes on for more chunks is a long one
+// Up to this many tiles, a CTA of the sort adds up the tiles' counts by itself
+// (2 KB of each: 1.5 us for 71 tiles, 5 for 192); above, a kernel of its own
+// scans them once for all CTAs (4 us with its launch).
+constexpr int kDirectTiles = 128;
+// Up to this many events are sorted by one CTA in one launch.
+constexpr int kSmallSort = 4096;
 
 // N consecutive elements in one access of N * sizeof(T) bytes.
 template <int BYTES> struct Raw;
@@ -58,8 +69,12 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int id_bytes, int64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Lookup: one thread for N columns of a row.
+// Lookup: a thread has kLookups pieces of N columns in flight, neighbouring
+// threads neighbouring pieces, in many small CTAs (a training batch of 287,928 rows
+// of 1,024 with the bf16 copy: 363 us with one piece a thread and 32 CTAs a
+// multiprocessor).
 // ---------------------------------------------------------------------------
+constexpr int kLookups = 4;
 template <typename TT, typename TO, int N, bool LOW>
 __global__ void __launch_bounds__(256) lookup_kernel(const TT* __restrict__ table, int64_t V, int dim,
                                                      int64_t table_stride, const void* __restrict__ ids,
@@ -67,29 +82,41 @@ __global__ void __launch_bounds__(256) lookup_kernel(const TT* __restrict__ tabl
                                                      TO* __restrict__ out, int width, int64_t out_stride,
                                                      bf16* __restrict__ low, int64_t low_stride) {
   const int units = width / N;
-  const int64_t total = rows * units, step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-    const int64_t t = i / units;
-    const int c = (int)(i - t * units) * N;
-    const int64_t id = id_at(ids, id_bytes, t);
+  const int64_t base = (int64_t)blockIdx.x * (256 * kLookups);
+  const RowOf where(base, units);
+  const int count = (int)min((int64_t)(256 * kLookups), rows * units - base);
+  Pack<TT, N> in[kLookups];
+  int64_t row[kLookups];
+  int col[kLookups];
+  bool any[kLookups];
+#pragma unroll
+  for (int i = 0; i < kLookups; ++i) {
+    const int off = i * 256 + (int)threadIdx.x;
+    any[i] = false;
+    if (off < count) {
+      const int r = where.rows_after(off);
+      row[i] = where.row0 + r;
+      col[i] = (where.col0 + off - r * units) * N;
+      const int64_t id = id_at(ids, id_bytes, row[i]);
+      any[i] = id >= 0 && id < V && col[i] < dim;     // N divides dim
+      if (any[i]) in[i].load(table + id * table_stride + col[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kLookups; ++i) {
+    if (i * 256 + (int)threadIdx.x >= count) break;
     float f[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) f[k] = 0.f;
-    if (id >= 0 && id < V && c < dim) {     // N divides dim
-      Pack<TT, N> a;
-      a.load(table + id * table_stride + c);
-#pragma unroll
-      for (int k = 0; k < N; ++k) f[k] = scale * to_f(a.v[k]);
-    }
+    for (int k = 0; k < N; ++k) f[k] = any[i] ? scale * to_f(in[i].v[k]) : 0.f;
     Pack<TO, N> o;
 #pragma unroll
     for (int k = 0; k < N; ++k) o.v[k] = from_f<TO>(f[k]);
-    o.store(out + t * out_stride + c);
+    o.store(out + row[i] * out_stride + col[i]);
     if (LOW) {
       Pack<bf16, N> l;
 #pragma unroll
       for (int k = 0; k < N; ++k) l.v[k] = from_f<bf16>(f[k]);
-      l.store(low + t * low_stride + c);
+      l.store(low + row[i] * low_stride + col[i]);
     }
   }
 }
@@ -111,19 +138,33 @@ struct PairSource {
   }
 };
 
-__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(PairSource src, int64_t T, int shift,
-                                                                 uint32_t* __restrict__ hist) {
+// A pass sorts by the digit (key >> shift) & mask.
+struct Pass {
+  int shift;
+  uint32_t mask;
+  __device__ __forceinline__ uint32_t digit(uint32_t key) const { return (key >> shift) & mask; }
+};
+
+// Counts the first pass's digits of every tile, and clears the counts of the
+// later passes and of the items to join.
+__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(PairSource src, int64_t T, Pass pass, int passes,
+                                                                 uint32_t* __restrict__ hist, int64_t pass_stride,
+                                                                 uint32_t* __restrict__ joins) {
   __shared__ uint32_t h[kDigits];
-  h[threadIdx.x] = 0;
+  if (threadIdx.x < kDigits) h[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) joins[threadIdx.x] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * kTile;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
+  for (int i = 0; i < kTile / kSortThreads; ++i) {
     const int64_t t = base + i * kSortThreads + threadIdx.x;
-    if (t < T) atomicAdd(&h[(src(t).x >> shift) & (kDigits - 1)], 1u);
+    if (t < T) atomicAdd(&h[pass.digit(src(t).x)], 1u);
   }
   __syncthreads();
-  hist[(int64_t)blockIdx.x * kDigits + threadIdx.x] = h[threadIdx.x];
+  if (threadIdx.x >= kDigits) return;
+  uint32_t* const out = hist + (int64_t)blockIdx.x * kDigits + threadIdx.x;
+  *out = h[threadIdx.x];
+  for (int p = 1; p < passes; ++p) out[p * pass_stride] = 0;
 }
 
 // One CTA a digit: hist[tile][digit] becomes the number of events with this
@@ -157,21 +198,10 @@ __global__ void __launch_bounds__(256) sort_scan_kernel(uint32_t* __restrict__ h
   if (threadIdx.x == 0) totals[blockIdx.x] = carry;
 }
 
-// Moves a tile's pairs to their places: the digit's first place (all lower
-// digits), plus its events in earlier tiles, earlier warps of the tile, and
-// earlier places of the warp.
-__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource src, int64_t T, int shift,
-                                                                    const uint32_t* __restrict__ hist,
-                                                                    const uint32_t* __restrict__ totals,
-                                                                    uint2* __restrict__ out) {
-  __shared__ uint32_t count[kSortWarps][kDigits];
-  __shared__ uint32_t first[kDigits];
-  __shared__ uint32_t warp_tot[kSortWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-#pragma unroll
-  for (int w = 0; w < kSortWarps; ++w) count[w][tid] = 0;
-  // exclusive scan of the digits' totals
-  const uint32_t x = totals[tid];
+// Exclusive prefix sum of x over the CTA's 32 warps.
+static_assert(kSortWarps == 32, "a warp's lanes scan the warps' totals");
+__device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t* warp_tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t v = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -180,72 +210,232 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
   }
   if (lane == 31) warp_tot[warp] = v;
   __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_tot[w];
-  first[tid] = before + v - x + hist[(int64_t)blockIdx.x * kDigits + tid];
-  // rank within the warp, whose events are consecutive
-  const int64_t base = (int64_t)blockIdx.x * kTile + warp * (32 * kPerThread);
-  uint2 pair[kPerThread];
-  uint32_t rank[kPerThread];
+  uint32_t w = lane < warp ? warp_tot[lane] : 0u;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t t = base + i * 32 + lane;
-    const bool in = t < T;
-    pair[i] = in ? src(t) : make_uint2(0, 0);
-    const uint32_t digit = (pair[i].x >> shift) & (kDigits - 1);
-    const uint32_t peers = __match_any_sync(0xffffffffu, in ? digit : 0x10000u);
+  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return w + v - x;
+}
+
+__device__ __forceinline__ void clear_counts(uint32_t (*count)[kDigits]) {
+  uint4* const p = reinterpret_cast<uint4*>(count[0]);
+#pragma unroll
+  for (int i = 0; i < kSortWarps * kDigits / 4 / kSortThreads; ++i)
+    p[i * kSortThreads + threadIdx.x] = make_uint4(0, 0, 0, 0);
+}
+// The thread's digit: its warps' counts become their first places, from `run` on.
+__device__ __forceinline__ void warps_first(uint32_t (*count)[kDigits], uint32_t run) {
+  uint32_t n[kSortWarps];
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) n[w] = count[w][threadIdx.x];
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    count[w][threadIdx.x] = run;
+    run += n[w];
+  }
+}
+
+// Stable ranks of N pairs a thread: warps hold consecutive runs of 32 N pairs,
+// pair i of a lane the one 32 i + lane places on.  rank: the pair's place among
+// those of its digit in its warp; count[warp][digit]: how many the warp has.
+template <int N>
+__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[N], const bool (&in)[N], uint32_t (&rank)[N],
+                                           uint32_t* count) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t peers = __match_any_sync(0xffffffffu, in[i] ? digit[i] : 0x10000u);
     const uint32_t ahead = __popc(peers & ((1u << lane) - 1u));
-    const uint32_t seen = in ? count[warp][digit] : 0u;
+    const uint32_t seen = in[i] ? count[digit[i]] : 0u;
     __syncwarp();
-    if (in && ahead == 0) count[warp][digit] = seen + __popc(peers);
+    if (in[i] && ahead == 0) count[digit[i]] = seen + __popc(peers);
     __syncwarp();
     rank[i] = seen + ahead;
   }
-  __syncthreads();
-  // over the warps: earlier ones of this digit, and the place where it begins
-  uint32_t run = first[tid];
+}
+
+// Moves a tile's pairs to their places: the digit's first place (all lower
+// digits), plus its events in earlier tiles, earlier warps of the tile, and
+// earlier places of the warp; and counts the next pass's digits of the tile
+// where each pair arrives.  DIRECT: hist holds the tiles' counts; otherwise their
+// prefix sums and, in totals, their sums.
+template <bool DIRECT>
+__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource src, int64_t T, Pass pass, int tiles,
+                                                                    const uint32_t* __restrict__ hist,
+                                                                    const uint32_t* __restrict__ totals,
+                                                                    uint2* __restrict__ out, Pass next,
+                                                                    uint32_t* __restrict__ next_hist) {
+  constexpr int N = kTile / kSortThreads, kGroups = kSortThreads * 4 / kDigits;
+  extern __shared__ uint32_t dyn[];
+  uint32_t(*const count)[kDigits] = reinterpret_cast<uint32_t(*)[kDigits]>(dyn);       // [kSortWarps]
+  __shared__ uint32_t warp_tot[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int64_t base = (int64_t)blockIdx.x * kTile + warp * (32 * N) + lane;
+  uint2 pair[N];
+  uint32_t digit[N], rank[N];
+  bool in[N];
 #pragma unroll
-  for (int w = 0; w < kSortWarps; ++w) {
-    const uint32_t n = count[w][tid];
-    count[w][tid] = run;
-    run += n;
+  for (int i = 0; i < N; ++i) {
+    in[i] = base + i * 32 < T;
+    pair[i] = in[i] ? src(base + i * 32) : make_uint2(0, 0);
+    digit[i] = pass.digit(pair[i].x);
   }
+  uint32_t all = 0, earlier = 0;        // this digit's events, and those of them in earlier tiles
+  if (DIRECT) {
+    // a thread adds four digits' counts of every kGroups-th tile
+    uint4 sum = make_uint4(0, 0, 0, 0), mine = make_uint4(0, 0, 0, 0);
+    const int group = tid / (kDigits / 4), d4 = tid % (kDigits / 4);
+    const uint4* const h = reinterpret_cast<const uint4*>(hist) + d4;
+    constexpr int kFlight = 9;
+    for (int t0 = group; t0 < tiles; t0 += kFlight * kGroups) {
+      uint4 v[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int t = min(t0 + i * kGroups, tiles - 1);
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                     : "l"(h + (int64_t)t * (kDigits / 4))
+                     : "memory");
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int t = t0 + i * kGroups;
+        const uint32_t there = t < tiles ? 0xffffffffu : 0u, m = t < (int)blockIdx.x ? there : 0u;
+        sum.x += v[i].x & there; sum.y += v[i].y & there; sum.z += v[i].z & there; sum.w += v[i].w & there;
+        mine.x += v[i].x & m; mine.y += v[i].y & m; mine.z += v[i].z & m; mine.w += v[i].w & m;
+      }
+    }
+    static_assert(2 * kGroups <= kSortWarps, "the groups' sums fit the counters");
+    reinterpret_cast<uint4*>(count[group])[d4] = sum;
+    reinterpret_cast<uint4*>(count[kGroups + group])[d4] = mine;
+    __syncthreads();
+    if (tid < kDigits)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        all += count[g][tid];
+        earlier += count[kGroups + g][tid];
+      }
+    __syncthreads();
+  } else if (tid < kDigits) {
+    all = totals[tid];
+    earlier = hist[(int64_t)blockIdx.x * kDigits + tid];
+  }
+  clear_counts(count);
+  const uint32_t run = block_prefix(all, warp_tot) + earlier;      // where the tile's events of this digit go
+  warp_ranks<N>(digit, in, rank, count[warp]);
+  __syncthreads();
+  if (tid < kDigits) warps_first(count, run);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t t = base + i * 32 + lane;
-    if (t < T) out[count[warp][(pair[i].x >> shift) & (kDigits - 1)] + rank[i]] = pair[i];
+  for (int i = 0; i < N; ++i) {
+    uint32_t at = 0xffffffffu;          // the next pass's counter of the pair
+    if (in[i]) {
+      const uint32_t to = count[warp][digit[i]] + rank[i];
+      out[to] = pair[i];
+      at = to / kTile * kDigits + next.digit(pair[i].x);
+    }
+    if (next_hist) {
+      // once for the warp's pairs that share it (a popular item's all do)
+      const uint32_t peers = __match_any_sync(0xffffffffu, at);
+      if (in[i] && (peers & ((1u << lane) - 1u)) == 0) atomicAdd(next_hist + at, (uint32_t)__popc(peers));
+    }
+  }
+}
+
+// All passes of T <= kSmallSort events, in shared memory.
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src, int T, int bits, int passes,
+                                                                  uint2* __restrict__ out,
+                                                                  uint32_t* __restrict__ joins) {
+  constexpr int N = kSmallSort / kSortThreads;
+  extern __shared__ uint32_t dyn[];
+  uint32_t(*const count)[kDigits] = reinterpret_cast<uint32_t(*)[kDigits]>(dyn);       // [kSortWarps]
+  uint2* const buf = reinterpret_cast<uint2*>(dyn + kSortWarps * kDigits);              // [kSmallSort]
+  __shared__ uint32_t warp_tot[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  if (tid < 2) joins[tid] = 0;
+  // consecutive events in consecutive warps, as few rounds as T takes
+  const int per = (T + kSortThreads - 1) / kSortThreads;
+  const int base = warp * (32 * per) + lane;
+  uint2 pair[N];
+  uint32_t digit[N], rank[N];
+  bool in[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    in[i] = i < per && base + i * 32 < T;
+    pair[i] = in[i] ? src(base + i * 32) : make_uint2(0, 0);
+  }
+  const int width = (bits + passes - 1) / passes;
+  for (int p = 0; p < passes; ++p) {
+    const Pass pass{p * width, (1u << width) - 1u};
+    clear_counts(count);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) digit[i] = pass.digit(pair[i].x);
+    warp_ranks<N>(digit, in, rank, count[warp]);
+    __syncthreads();
+    uint32_t all = 0;
+    if (tid < kDigits)
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) all += count[w][tid];
+    const uint32_t run = block_prefix(all, warp_tot);
+    if (tid < kDigits) warps_first(count, run);
+    __syncthreads();
+    uint2* const to = p + 1 == passes ? out : buf;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (in[i]) to[count[warp][digit[i]] + rank[i]] = pair[i];
+    if (p + 1 == passes) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (in[i]) pair[i] = buf[base + i * 32];
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
 // Rows form: how many items begin before each chunk
 // ---------------------------------------------------------------------------
-// heads[c] = items whose first event lies in chunk c.
-__global__ void __launch_bounds__(256) heads_kernel(const uint2* __restrict__ pairs, int64_t T, uint32_t V,
-                                                    int64_t chunks, uint32_t* __restrict__ heads) {
-  const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t t = c * kChunk + (threadIdx.x & 31);
+// heads[c]: items whose first event lies in an earlier chunk of chunk c's
+// kSuper events; supers[s]: in kSuper events number s.
+__global__ void __launch_bounds__(kSuper) heads_kernel(const uint2* __restrict__ pairs, int64_t T, uint32_t V,
+                                                       int64_t chunks, uint32_t* __restrict__ heads,
+                                                       uint32_t* __restrict__ supers) {
+  __shared__ uint32_t warp_n[kSuper / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kSuper + threadIdx.x;
   bool head = false;
   if (t < T) {
     const uint32_t k = pairs[t].x;
     head = k < V && (t == 0 || pairs[t - 1].x != k);
   }
   const uint32_t n = __popc(__ballot_sync(0xffffffffu, head));
-  if (c < chunks && (threadIdx.x & 31) == 0) heads[c] = n;
+  if (lane == 0) warp_n[warp] = n;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t x = warp_n[lane];
+    uint32_t v = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    const int64_t c = (int64_t)blockIdx.x * (kSuper / kChunk) + lane;
+    if (c < chunks) heads[c] = v - x;
+    if (lane == 31) supers[blockIdx.x] = v;
+  }
 }
 
-// heads becomes its exclusive prefix sum; *num_rows the number of items.  One CTA.
-__global__ void __launch_bounds__(1024) heads_scan_kernel(uint32_t* __restrict__ heads, int64_t chunks,
-                                                          int64_t* __restrict__ num_rows) {
+// supers becomes its exclusive prefix sum; *num_rows the number of items.  One CTA.
+__global__ void __launch_bounds__(1024) supers_kernel(uint32_t* __restrict__ supers, int64_t n,
+                                                      int64_t* __restrict__ num_rows) {
   __shared__ uint32_t warp_tot[32];
   __shared__ uint32_t carry;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) carry = 0;
   __syncthreads();
-  for (int64_t base = 0; base < chunks; base += 1024) {
+  for (int64_t base = 0; base < n; base += 1024) {
     const int64_t i = base + threadIdx.x;
-    const uint32_t x = i < chunks ? heads[i] : 0u;
+    const uint32_t x = i < n ? supers[i] : 0u;
     uint32_t v = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -256,7 +446,7 @@ __global__ void __launch_bounds__(1024) heads_scan_kernel(uint32_t* __restrict__
     __syncthreads();
     uint32_t before = carry;
     for (int w = 0; w < warp; ++w) before += warp_tot[w];
-    if (i < chunks) heads[i] = before + v - x;
+    if (i < n) supers[i] = before + v - x;
     __syncthreads();
     if (threadIdx.x == 1023) carry = before + v;
     __syncthreads();
@@ -276,23 +466,45 @@ struct SumArgs {
   float scale;
   float* dst;                 // dtable or rows
   int64_t dst_stride;
-  const uint32_t* heads;      // rows form: items before each chunk; else NULL
+  const uint32_t *heads, *supers;      // rows form: items before each chunk; else NULL
   int64_t* row_ids;
   float* partial;             // [chunks][2][dim]
+  // Items that cross chunks, by the chunk where they begin: joins[0] short ones
+  // from the front of a list of [chunks], joins[1] long ones from its end.
+  uint32_t* joins;
+  __device__ __forceinline__ uint32_t* list() const { return joins + 2; }
+  // Items that begin before chunk c.
+  __device__ __forceinline__ int64_t before(int64_t c) const {
+    return (int64_t)supers[c / (kSuper / kChunk)] + heads[c];
+  }
 };
 
-// Adds (dense) or writes (rows form) an item's sum.
-template <int N>
-__device__ __forceinline__ void put_sum(const SumArgs& a, int64_t row, int col, const float (&f)[N]) {
-  float* const p = a.dst + row * a.dst_stride + col;
+template <int N> __device__ __forceinline__ void load_f(const float* p, float (&f)[N]) {
+  constexpr int M = N > 4 ? 4 : N;
 #pragma unroll
-  for (int k = 0; k < N; ++k) p[k] = a.heads ? a.scale * f[k] : p[k] + a.scale * f[k];
+  for (int i = 0; i < N; i += M) {
+    Pack<float, M> a;
+    a.load(p + i);
+#pragma unroll
+    for (int k = 0; k < M; ++k) f[i + k] = a.v[k];
+  }
+}
+template <int N> __device__ __forceinline__ void store_f(float* p, const float (&f)[N]) {
+  constexpr int M = N > 4 ? 4 : N;
+#pragma unroll
+  for (int i = 0; i < N; i += M) {
+    Pack<float, M> a;
+#pragma unroll
+    for (int k = 0; k < M; ++k) a.v[k] = f[i + k];
+    a.store(p + i);
+  }
 }
 
 // A warp sums a chunk's columns [32 N y, 32 N (y + 1)); a lane owns N of them.
 // partial[c][0]: the sum of the item that came over from the chunk before;
 // partial[c][1]: of the one that begins in the chunk and goes on after it.
-template <typename T, int N>
+// ROWS: items are written to their places in the rows form, else added.
+template <typename T, int N, bool ROWS>
 __global__ void __launch_bounds__(256) sum_kernel(SumArgs a, const T* __restrict__ dout) {
   const int lane = threadIdx.x & 31;
   const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -302,81 +514,180 @@ __global__ void __launch_bounds__(256) sum_kernel(SumArgs a, const T* __restrict
   const uint2 mine = lane < n ? a.pairs[t0 + lane] : make_uint2(a.V, 0);
   const uint32_t before = t0 > 0 ? a.pairs[t0 - 1].x : a.V;
   const uint32_t after = t0 + n < a.T ? a.pairs[t0 + n].x : a.V;
-  uint32_t left = __shfl_up_sync(0xffffffffu, mine.x, 1);
+  const uint32_t far = t0 + (kAlone + 1) * kChunk < a.T ? a.pairs[t0 + (kAlone + 1) * kChunk].x : a.V;
+  uint32_t left = __shfl_up_sync(0xffffffffu, mine.x, 1), right = __shfl_down_sync(0xffffffffu, mine.x, 1);
   if (lane == 0) left = before;
+  if (lane == n - 1) right = after;
   const bool real = mine.x < a.V;
   const uint32_t begins = __ballot_sync(0xffffffffu, real && left != mine.x);   // an item's first event
+  const uint32_t ends = __ballot_sync(0xffffffffu, real && right != mine.x);    // an item's last event
   const int count = __popc(__ballot_sync(0xffffffffu, real));   // padding sorts last
   if (count == 0) return;
   const int col = ((int)blockIdx.y * 32 + lane) * N;
   const bool live = col < a.dim;
-  const int64_t first_row = a.heads ? (int64_t)a.heads[c] : 0;
+  const T* const src = dout + (live ? col : 0);
+  float* const dst = a.dst + (live ? col : 0);
+  const int64_t first_row = ROWS ? a.before(c) - 1 : 0;
   float acc[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) acc[k] = 0.f;
-  bool open = (begins & 1u) == 0;       // the running item began before this chunk
-  int started = 0;                      // items begun in this chunk so far
-  for (int j = 0; j < count; ++j) {
-    const uint32_t key = __shfl_sync(0xffffffffu, mine.x, j), ev = __shfl_sync(0xffffffffu, mine.y, j);
-    if ((begins >> j) & 1u) ++started;
-    if (live) {
-      Pack<T, N> p;
-      p.load(dout + (int64_t)ev * a.dout_stride + col);
+#pragma unroll 1
+  for (int j0 = 0; j0 < count; j0 += kBatch) {
+    Pack<T, N> row[kBatch];
+    float old[ROWS ? 1 : kBatch][N];
 #pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] += to_f(p.v[k]);
-    }
-    const bool last = j + 1 == count;
-    const bool ends = last ? !(count == n && after == key) : ((begins >> (j + 1)) & 1u);
-    if (!ends && !last) continue;
-    const int64_t row = a.heads ? first_row + started - 1 : (int64_t)key;
-    if (live) {
-      if (open || !ends) {
-        float* const w = a.partial + (c * 2 + (open ? 0 : 1)) * a.dim + col;
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = acc[k];
-      } else {
-        put_sum<N>(a, row, col, acc);
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i;
+      const uint32_t key = __shfl_sync(0xffffffffu, mine.x, j & 31), ev = __shfl_sync(0xffffffffu, mine.y, j & 31);
+      if (j < count && live) {
+        row[i].load(src + (int64_t)ev * a.dout_stride);
+        // what the gradient holds of an item that begins and ends in this chunk
+        if (!ROWS && (ends >> j & 1u) && (begins & (0xffffffffu >> (31 - j)))) load_f<N>(dst + (int64_t)key * a.dst_stride, old[i]);
       }
     }
-    if (a.heads && !open && blockIdx.y == 0 && lane == 0) a.row_ids[row] = key;
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] = 0.f;
-    open = false;
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i;
+      if (j >= count) break;
+      const uint32_t key = __shfl_sync(0xffffffffu, mine.x, j);
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] += to_f(row[i].v[k]);
+      const bool end = ends >> j & 1u;
+      if (!end && j + 1 < count) continue;
+      const uint32_t begun = begins & (0xffffffffu >> (31 - j));      // items begun so far
+      if (!begun || !end) {
+        if (live) store_f<N>(a.partial + (c * 2 + (begun ? 1 : 0)) * a.dim + col, acc);
+        if (begun && blockIdx.y == 0 && lane == 0) {
+          const int is_long = far == key;
+          const int64_t i = atomicAdd(a.joins + is_long, 1u);
+          a.list()[is_long ? a.chunks - 1 - i : i] = (uint32_t)c;
+        }
+      } else if (live) {
+        const int64_t at = ROWS ? first_row + __popc(begun) : (int64_t)key;
+        float f[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] = ROWS ? a.scale * acc[k] : old[ROWS ? 0 : i][k] + a.scale * acc[k];
+        store_f<N>(dst + at * a.dst_stride, f);
+      }
+      if (ROWS && begun && blockIdx.y == 0 && lane == 0) a.row_ids[first_row + __popc(begun)] = key;
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    }
   }
 }
 
-// A CTA for a chunk: where the chunk's last item begins in it and goes on, adds
-// up the item's partial sums.
-__global__ void __launch_bounds__(256) join_kernel(SumArgs a) {
-  __shared__ float strip[8][32];
-  const int64_t c = blockIdx.x, t0 = c * kChunk, end = t0 + kChunk;
-  if (end >= a.T) return;
-  const uint32_t key = a.pairs[end].x;
-  if (key >= a.V || a.pairs[end - 1].x != key) return;               // nothing goes on
-  if (a.pairs[t0].x == key && t0 > 0 && a.pairs[t0 - 1].x == key) return;    // it began earlier
-  // the chunks that the item came over to: c + 1 .. last (a chunk's first
-  // event is the item's as long as the chunk's index does not pass it)
-  int64_t lo = c + 1, hi = a.chunks;            // first chunk that does not begin with the item is in (lo, hi]
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.pairs[mid * kChunk].x == key) lo = mid; else hi = mid;
-  }
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t row = a.heads ? (int64_t)a.heads[c + 1] - 1 : (int64_t)key;
-  for (int base = 0; base < a.dim; base += 32) {
-    const int col = base + lane;
-    float t = 0.f;
-    if (col < a.dim) {
-      if (w == 0) t = a.partial[(c * 2 + 1) * a.dim + col];
-      for (int64_t i = c + 1 + w; i <= lo; i += 8) t += a.partial[i * 2 * a.dim + col];
+// Where the item ends that begins in chunk c and goes on: the last chunk that
+// begins with its id.  The warp's lanes probe the next 32 chunks, then 32
+// places of what is left, until the places are neighbours.
+__device__ __forceinline__ int64_t last_chunk(const SumArgs& a, int64_t c, uint32_t key) {
+  const int lane = threadIdx.x & 31;
+  int64_t last = c + 1, step = 1, end = a.chunks;
+  while (true) {
+    const int64_t p = last + step * (lane + 1);
+    const uint32_t same = __ballot_sync(0xffffffffu, p < end && a.pairs[p * kChunk].x == key);
+    const int run = __popc(same);             // the ids are sorted: a run of lanes from the first
+    last += step * run;
+    if (run == 32) {
+      step = (end - last + 31) / 32;          // at least 1: last is a chunk
+    } else if (step == 1) {
+      return last;
+    } else {
+      end = min(end, last + step);
+      step = (step + 31) / 32;
     }
-    strip[w][lane] = t;
-    __syncthreads();
-    if (w == 0 && col < a.dim) {
+  }
+}
+
+// N floats, loaded where the program says (volatile: the compiler would move
+// each load of a batch down to its use, and wait for every one of them).
+template <int N> __device__ __forceinline__ void load_now(const float* p, float (&f)[N]) {
+  if constexpr (N >= 4) {
 #pragma unroll
-      for (int k = 1; k < 8; ++k) t += strip[k][lane];
-      const float f[1] = {t};
-      put_sum<1>(a, row, col, f);
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(f[i]), "=f"(f[i + 1]), "=f"(f[i + 2]), "=f"(f[i + 3])
+                   : "l"(p + i)
+                   : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "l"(p) : "memory");
+  } else {
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(f[0]) : "l"(p) : "memory");
+  }
+}
+
+// Adds the partial sums of chunks first, first + STRIDE, ... up to last (at
+// least one), kFlight of them in flight; places past the last load that one again.
+template <int N, int STRIDE, int kFlight>
+__device__ __forceinline__ void add_partials(const SumArgs& a, int64_t first, int64_t last, int col, float (&acc)[N]) {
+  const float* p = a.partial + first * 2 * a.dim + col;
+  const int64_t step = (int64_t)STRIDE * 2 * a.dim;
+  for (int64_t left = (last - first) / STRIDE + 1; left > 0; left -= kFlight, p += kFlight * step) {
+    float f[kFlight][N];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) load_now<N>(p + min((int64_t)i, left - 1) * step, f[i]);
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i)
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] += i < left ? f[i][k] : 0.f;
+  }
+}
+
+template <int N, bool ROWS>
+__device__ __forceinline__ void put_joined(const SumArgs& a, int64_t c, uint32_t key, int col, const float (&acc)[N]) {
+  const int64_t at = ROWS ? a.before(c + 1) - 1 : (int64_t)key;
+  float* const p = a.dst + at * a.dst_stride + col;
+  float f[N];
+  if (!ROWS) load_f<N>(p, f);
+#pragma unroll
+  for (int k = 0; k < N; ++k) f[k] = ROWS ? a.scale * acc[k] : f[k] + a.scale * acc[k];
+  store_f<N>(p, f);
+}
+
+// Joins the partial sums of the listed items, columns [32 N y, 32 N (y + 1)) of
+// each: CTAs [0, longs) the long items, one at a time, whose warps add every
+// kJoinWarps-th chunk; the others the short ones, a warp each.
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+template <int N, bool ROWS>
+__global__ void __launch_bounds__(kJoinThreads, N > 4 ? 2 : 3) join_kernel(SumArgs a, unsigned longs) {
+  __shared__ float strip[kJoinWarps][32 * N];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int col = ((int)blockIdx.y * 32 + lane) * N;
+  const bool live = col < a.dim;
+  if (blockIdx.x >= longs) {
+    const uint32_t items = a.joins[0];
+    for (uint32_t i = (blockIdx.x - longs) * kJoinWarps + w; i < items; i += (gridDim.x - longs) * kJoinWarps) {
+      const int64_t c = a.list()[i];
+      const uint32_t key = a.pairs[(c + 1) * kChunk].x;
+      const int64_t last = last_chunk(a, c, key);
+      if (!live) continue;
+      float acc[N];
+      load_f<N>(a.partial + (c * 2 + 1) * a.dim + col, acc);
+      add_partials<N, 1, 4>(a, c + 1, last, col, acc);
+      put_joined<N, ROWS>(a, c, key, col, acc);
+    }
+    return;
+  }
+  const uint32_t items = a.joins[1];
+  for (uint32_t i = blockIdx.x; i < items; i += longs) {
+    const int64_t c = a.list()[a.chunks - 1 - i];
+    const uint32_t key = a.pairs[(c + 1) * kChunk].x;
+    const int64_t last = last_chunk(a, c, key);
+    float acc[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    if (live) {
+      if (w == 0) load_f<N>(a.partial + (c * 2 + 1) * a.dim + col, acc);
+      add_partials<N, kJoinWarps, 8>(a, c + 1 + w, last, col, acc);     // longer than kJoinWarps chunks
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) strip[w][k * 32 + lane] = acc[k];
+    __syncthreads();
+    if (w == 0 && live) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int o = 1; o < kJoinWarps; ++o) acc[k] += strip[o][k * 32 + lane];
+      put_joined<N, ROWS>(a, c, key, col, acc);
     }
     __syncthreads();
   }
@@ -390,19 +701,22 @@ bool vec_ok(int64_t n, const void* p, int64_t bytes, int64_t stride, int64_t a, 
 }
 
 struct BwdLayout {
-  size_t a, b, hist, totals, heads, partial, total;
-  int64_t tiles, chunks;
+  size_t a, b, hist, totals, heads, supers, joins, partial, total;
+  int64_t tiles, chunks, nsupers;
 };
 BwdLayout bwd_layout(int64_t T, int dim) {
   BwdLayout l;
   l.tiles = (T + kTile - 1) / kTile;
   l.chunks = (T + kChunk - 1) / kChunk;
+  l.nsupers = (T + kSuper - 1) / kSuper;
   l.a = 0;
   l.b = align_up(l.a + (size_t)T * 8, 256);
   l.hist = align_up(l.b + (size_t)T * 8, 256);
-  l.totals = align_up(l.hist + (size_t)l.tiles * kDigits * 4, 256);
+  l.totals = align_up(l.hist + (size_t)l.tiles * kDigits * 4 * kMaxPasses, 256);
   l.heads = align_up(l.totals + kDigits * 4, 256);
-  l.partial = align_up(l.heads + (size_t)l.chunks * 4, 256);
+  l.supers = align_up(l.heads + (size_t)l.chunks * 4, 256);
+  l.joins = align_up(l.supers + (size_t)l.nsupers * 4, 256);
+  l.partial = align_up(l.joins + 8 + (size_t)l.chunks * 4, 256);
   l.total = align_up(l.partial + (size_t)l.chunks * 2 * (size_t)dim * 4, 256);
   return l;
 }
@@ -418,21 +732,38 @@ hstu_status check_ids(const void* ids, int32_t id_bytes, int64_t T) {
 }
 hstu_status check_dtype(int32_t t) { return t == HSTU_F32 || t == HSTU_BF16 ? HSTU_OK : HSTU_ERR_INVALID; }
 
-template <typename T>
-cudaError_t launch_sum(const SumArgs& a, const void* dout, int n, cudaStream_t s) {
-  const T* p = static_cast<const T*>(dout);
-  const dim3 grid((unsigned)((a.chunks + 7) / 8), (unsigned)((a.dim + 32 * n - 1) / (32 * n)));
-  if (n == 4) sum_kernel<T, 4><<<grid, 256, 0, s>>>(a, p);
-  else if (n == 2) sum_kernel<T, 2><<<grid, 256, 0, s>>>(a, p);
-  else sum_kernel<T, 1><<<grid, 256, 0, s>>>(a, p);
+template <typename T, int N, bool ROWS>
+cudaError_t launch_sum_n(const SumArgs& a, const void* dout, cudaStream_t s) {
+  const unsigned slices = (unsigned)((a.dim + 32 * N - 1) / (32 * N));
+  sum_kernel<T, N, ROWS><<<dim3((unsigned)((a.chunks + 7) / 8), slices), 256, 0, s>>>(a, static_cast<const T*>(dout));
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.chunks > 1) {
-    join_kernel<<<(unsigned)a.chunks, 256, 0, s>>>(a);
+    // CTAs for as many items as there can be, at most one (long) and two
+    // (short) a multiprocessor
+    const int64_t sms = sm_count(), most = (sms + slices - 1) / slices;
+    const int64_t longs = std::min(most, (a.chunks + kAlone - 1) / kAlone);
+    const int64_t shorts = std::min(2 * most, (a.chunks + kJoinWarps - 1) / kJoinWarps);
+    join_kernel<N, ROWS><<<dim3((unsigned)(longs + shorts), slices), kJoinThreads, 0, s>>>(a, (unsigned)longs);
     count_launch();
     e = cudaGetLastError();
   }
   return e;
+}
+// N columns a lane: 16 bytes of dout where alignment and width allow, fewer
+// rather than idle lanes for narrow rows.
+template <typename T, bool ROWS>
+cudaError_t launch_sum(const SumArgs& a, const void* dout, cudaStream_t s) {
+  constexpr int kMost = 16 / (int)sizeof(T);
+  int n = kMost;
+  while (n > 1 && !(vec_ok(n, dout, sizeof(T), a.dout_stride, a.dim, a.dim) &&
+                    vec_ok(n < 4 ? n : 4, a.dst, 4, a.dst_stride, a.dim, a.dim) && (n == 2 || a.dim > 16 * n)))
+    n >>= 1;
+  if constexpr (kMost == 8)
+    if (n == 8) return launch_sum_n<T, 8, ROWS>(a, dout, s);
+  return n == 4 ? launch_sum_n<T, 4, ROWS>(a, dout, s)
+         : n == 2 ? launch_sum_n<T, 2, ROWS>(a, dout, s)
+                  : launch_sum_n<T, 1, ROWS>(a, dout, s);
 }
 
 // The gradient in either form; rows form when row_ids is given.
@@ -442,30 +773,49 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
   const BwdLayout l = bwd_layout(T, dim);
   char* const base = static_cast<char*>(ws);
   uint2* pairs[2] = {reinterpret_cast<uint2*>(base + l.a), reinterpret_cast<uint2*>(base + l.b)};
-  uint32_t* hist = reinterpret_cast<uint32_t*>(base + l.hist);
-  uint32_t* totals = reinterpret_cast<uint32_t*>(base + l.totals);
-  uint32_t* heads = reinterpret_cast<uint32_t*>(base + l.heads);
+  uint32_t* const hist = reinterpret_cast<uint32_t*>(base + l.hist);
+  uint32_t* const totals = reinterpret_cast<uint32_t*>(base + l.totals);
+  uint32_t* const joins = reinterpret_cast<uint32_t*>(base + l.joins);
   int bits = 0;
-  while (bits < 32 && ((uint64_t)V >> bits) != 0) ++bits;        // keys are 0 .. V
-  int cur = 0;
+  while (((uint64_t)V >> bits) != 0) ++bits;                      // keys are 0 .. V
+  const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes;
   PairSource src{nullptr, ids, id_bytes, (uint32_t)V};
-  for (int shift = 0; shift < bits; shift += 8) {
-    sort_hist_kernel<<<(unsigned)l.tiles, kSortThreads, 0, s>>>(src, T, shift, hist);
-    sort_scan_kernel<<<kDigits, 256, 0, s>>>(hist, (int)l.tiles, totals);
-    sort_scatter_kernel<<<(unsigned)l.tiles, kSortThreads, 0, s>>>(src, T, shift, hist, totals, pairs[cur]);
-    count_launch(3);
-    src.pairs = pairs[cur];
-    cur ^= 1;
-    const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (T <= kSmallSort) {
+    constexpr int kBytes = kSortWarps * kDigits * 4 + kSmallSort * 8;
+    e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-  }
-  if (row_ids) {
-    heads_kernel<<<(unsigned)((l.chunks + 7) / 8), 256, 0, s>>>(src.pairs, T, (uint32_t)V, l.chunks, heads);
-    heads_scan_kernel<<<1, 1024, 0, s>>>(heads, l.chunks, num_rows);
-    count_launch(2);
-    const cudaError_t e = cudaGetLastError();
+    sort_small_kernel<<<1, kSortThreads, kBytes, s>>>(src, (int)T, bits, passes, pairs[0], joins);
+    count_launch();
+    src.pairs = pairs[0];
+  } else {
+    const int64_t stride = l.tiles * kDigits;
+    constexpr int kBytes = kSortWarps * kDigits * 4;
+    const bool direct = l.tiles <= kDirectTiles;
+    e = cudaFuncSetAttribute(direct ? sort_scatter_kernel<true> : sort_scatter_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
+    const auto pass = [&](int p) { return Pass{p * width, (1u << width) - 1u}; };
+    sort_hist_kernel<<<(unsigned)l.tiles, kSortThreads, 0, s>>>(src, T, pass(0), passes, hist, stride, joins);
+    count_launch();
+    for (int p = 0; p < passes; ++p) {
+      uint32_t* const h = hist + p * stride;
+      uint32_t* const next = p + 1 < passes ? h + stride : nullptr;
+      if (direct) {
+        sort_scatter_kernel<true><<<(unsigned)l.tiles, kSortThreads, kBytes, s>>>(src, T, pass(p), (int)l.tiles, h, totals,
+                                                                             pairs[p & 1], pass(p + 1), next);
+      } else {
+        sort_scan_kernel<<<kDigits, 256, 0, s>>>(h, (int)l.tiles, totals);
+        count_launch();
+        sort_scatter_kernel<false><<<(unsigned)l.tiles, kSortThreads, kBytes, s>>>(src, T, pass(p), (int)l.tiles, h, totals,
+                                                                              pairs[p & 1], pass(p + 1), next);
+      }
+      count_launch();
+      src.pairs = pairs[p & 1];
+    }
   }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   SumArgs a;
   a.pairs = src.pairs;
   a.T = T;
@@ -476,13 +826,21 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
   a.scale = scale;
   a.dst = dst;
   a.dst_stride = dst_stride;
-  a.heads = row_ids ? heads : nullptr;
+  a.heads = reinterpret_cast<uint32_t*>(base + l.heads);
+  a.supers = reinterpret_cast<uint32_t*>(base + l.supers);
   a.row_ids = row_ids;
   a.partial = reinterpret_cast<float*>(base + l.partial);
-  const int64_t es = dtype_size(dout_dtype);
-  int n = 4;
-  while (n > 1 && !vec_ok(n, dout, es, dout_stride, dim, dim)) n >>= 1;
-  return dout_dtype == HSTU_BF16 ? launch_sum<bf16>(a, dout, n, s) : launch_sum<float>(a, dout, n, s);
+  a.joins = joins;
+  if (!row_ids)
+    return dout_dtype == HSTU_BF16 ? launch_sum<bf16, false>(a, dout, s) : launch_sum<float, false>(a, dout, s);
+  heads_kernel<<<(unsigned)l.nsupers, kSuper, 0, s>>>(src.pairs, T, (uint32_t)V, l.chunks,
+                                                      reinterpret_cast<uint32_t*>(base + l.heads),
+                                                      reinterpret_cast<uint32_t*>(base + l.supers));
+  supers_kernel<<<1, 1024, 0, s>>>(reinterpret_cast<uint32_t*>(base + l.supers), l.nsupers, num_rows);
+  count_launch(2);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return dout_dtype == HSTU_BF16 ? launch_sum<bf16, true>(a, dout, s) : launch_sum<float, true>(a, dout, s);
 }
 
 template <typename TT, typename TO, bool LOW>
@@ -494,8 +852,9 @@ cudaError_t launch_lookup(const void* table, int64_t V, int dim, int64_t table_s
                     vec_ok(n, out, sizeof(TO), out_stride, dim, width) &&
                     (!LOW || vec_ok(n, low, 2, low_stride, dim, width))))
     n >>= 1;
-  const int64_t want = (T * (width / n) + 255) / 256, cap = (int64_t)sm_count() * 32;
-  const unsigned grid = (unsigned)(want < cap ? want : cap);
+  const int64_t ctas = (T * (width / n) + 256 * kLookups - 1) / (256 * kLookups);
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)ctas;
   const TT* t = static_cast<const TT*>(table);
   TO* o = static_cast<TO*>(out);
   bf16* l = static_cast<bf16*>(low);
