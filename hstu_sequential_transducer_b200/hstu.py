@@ -453,20 +453,28 @@ _DTYPE_IDS = {torch.float32: HSTU_F32, torch.bfloat16: HSTU_BF16}
 
 def _rows(where, name, t, rows, width, dtype, device):
     """Checks a [rows][width] tensor with unit inner stride; returns its row stride."""
-    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != rows or \
-            t.shape[1] != width or (t.stride(1) != 1 and width > 1):
-        raise ValueError(f"{where}: {name} must be [{rows}][{width}] {dtype} on {device} with unit "
-                         f"inner stride, got {tuple(t.shape)} {t.dtype} on {t.device}, strides "
-                         f"{t.stride()}")
-    return t.stride(0) if rows > 1 else max(t.stride(0), width)
+    if t.dtype is dtype and t.shape == (rows, width) and t.device == device:
+        st = t.stride()
+        if st[1] == 1 or width == 1:
+            return st[0] if rows > 1 or st[0] > width else width
+    raise ValueError(f"{where}: {name} must be [{rows}][{width}] {dtype} on {device} with unit inner "
+                     f"stride, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
 
 
 def _flat(where, name, t, shape, dtype, device):
-    """Checks a contiguous tensor of this shape (a None is let through)."""
-    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or
-                          not t.is_contiguous()):
-        raise ValueError(f"{where}: {name} must be contiguous {tuple(shape)} {dtype} on {device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    """Checks a contiguous tensor of this shape; returns its address (None for a None)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{where}: {name} must be contiguous {tuple(shape)} {dtype} on {device}, got "
+                     f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+
+
+# The current stream's handle: torch.cuda.current_stream() makes a Stream object
+# of it at every call, which takes as long as the launch itself.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _launch(where, device, stream, f, *args, ws_bytes=None):
@@ -475,21 +483,27 @@ def _launch(where, device, stream, f, *args, ws_bytes=None):
     two calls, streams or captured graphs share one."""
     if device.type != "cuda":
         raise ValueError(f"{where}: needs CUDA tensors, got {device}")
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _launch(where, device, stream, f, *args, ws_bytes=ws_bytes)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    if s.device_index != device.index:
-        raise ValueError(f"{where}: the stream belongs to cuda:{s.device_index}, the tensors to {device}")
-    if ws_bytes is None:
-        _check(f(*args, s.cuda_stream), where)
-        return
     if stream is None:
-        ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=device)
+        s = _raw_stream(index)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
     else:
-        with torch.cuda.stream(stream):
-            ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=device)
-    _check(f(*args, ws.data_ptr(), ws_bytes, s.cuda_stream), where)
+        if stream.device_index != index:
+            raise ValueError(f"{where}: the stream belongs to cuda:{stream.device_index}, the tensors "
+                             f"to {device}")
+        s, ws = stream.cuda_stream, None
+        if ws_bytes:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    if ws_bytes is None:
+        status = f(*args, s)
+    else:
+        status = f(*args, None if ws is None else ws.data_ptr(), ws_bytes, s)
+    if status:
+        raise HSTUError(status, where)
 
 
 # ----------------------------------------------------------------------------
@@ -597,10 +611,13 @@ class BlockNorm:
         if self.post not in _NORMS or self.pre not in _NORMS or self.gate_act not in _GATES:
             raise ValueError(f"{where}: unknown norm or gate activation: {self.post}, {self.pre}, "
                              f"{self.gate_act}")
-        p = [getattr(self, n) for n in _PARAMS]
-        for n, t in zip(_PARAMS, p):
-            _flat(where, n, t, (cfg.d_model,), torch_dtype(cfg.dtype), device)
-        return CBlockNorm(_NORMS[self.post], _NORMS[self.pre], _GATES[self.gate_act], 0, *map(ptr, p))
+        shape, dt = (cfg.d_model,), torch_dtype(cfg.dtype)
+        return CBlockNorm(_NORMS[self.post], _NORMS[self.pre], _GATES[self.gate_act], 0,
+                          _flat(where, "post_gamma", self.post_gamma, shape, dt, device),
+                          _flat(where, "post_beta", self.post_beta, shape, dt, device),
+                          _flat(where, "res_scale", self.res_scale, shape, dt, device),
+                          _flat(where, "pre_gamma", self.pre_gamma, shape, dt, device),
+                          _flat(where, "pre_beta", self.pre_beta, shape, dt, device))
 
 
 @dataclass
@@ -618,10 +635,9 @@ class BlockNormGrads:
         return BlockNormGrads(*(z(getattr(bn, n)) for n in _PARAMS))
 
     def c(self, cfg, where, device) -> CBlockNormGrads:
-        p = [getattr(self, n) for n in _PARAMS]
-        for n, t in zip(_PARAMS, p):
-            _flat(where, "grads." + n, t, (cfg.d_model,), torch.float32, device)
-        return CBlockNormGrads(*map(ptr, p))
+        shape = (cfg.d_model,)
+        return CBlockNormGrads(*[_flat(where, n, getattr(self, n), shape, torch.float32, device)
+                                 for n in _PARAMS])
 
 
 def block_norm_fwd(cfg, bn: BlockNorm, x, b=None, gate=None, y=None, h=None, stats=None, want_h=True,
@@ -638,13 +654,12 @@ def block_norm_fwd(cfg, bn: BlockNorm, x, b=None, gate=None, y=None, h=None, sta
         y, gate = x, None
     elif y is None:
         y = torch.empty_like(x)
-    for n, t, ty in (("x", x, io), ("b", b, io), ("y", y, io), ("h", h, dt)):
-        _flat(where, n, t, (T, d), ty, dev)
-    _flat(where, "stats", stats, (T, 4), torch.float32, dev)
+    shape = (T, d)
     gs = 0 if gate is None else _rows(where, "gate", gate, T, d, dt, dev)
     _launch(where, dev, stream, lib().hstu_block_norm_fwd, ctypes.byref(cfg),
-            ctypes.byref(bn.c(cfg, where, dev)), x.data_ptr(), ptr(b), ptr(gate), gs, T, y.data_ptr(),
-            ptr(h), ptr(stats))
+            ctypes.byref(bn.c(cfg, where, dev)), _flat(where, "x", x, shape, io, dev),
+            _flat(where, "b", b, shape, io, dev), ptr(gate), gs, T, _flat(where, "y", y, shape, io, dev),
+            _flat(where, "h", h, shape, dt, dev), _flat(where, "stats", stats, (T, 4), torch.float32, dev))
     return y, h
 
 
@@ -664,17 +679,17 @@ def block_norm_bwd(cfg, bn: BlockNorm, y, b, gate, stats, dy=None, dh=None, dx=N
         raise ValueError(f"{where}: dgate needs gate")
     if dx is None:
         dx = torch.empty(T, d, dtype=io, device=dev)
-    for n, t, ty in (("y", y, io), ("b", b, io), ("dy", dy, io), ("dh", dh, io), ("dx", dx, io),
-                     ("db", db, dt)):
-        _flat(where, n, t, (T, d), ty, dev)
-    _flat(where, "stats", stats, (T, 4), torch.float32, dev)
+    shape = (T, d)
     gs = 0 if gate is None else _rows(where, "gate", gate, T, d, dt, dev)
     dgs = 0 if dgate is None else _rows(where, "dgate", dgate, T, d, dt, dev)
     L = lib()
     g = None if grads is None else ctypes.byref(grads.c(cfg, where, dev))
     _launch(where, dev, stream, L.hstu_block_norm_bwd, ctypes.byref(cfg),
-            ctypes.byref(bn.c(cfg, where, dev)), ptr(y), ptr(b), ptr(gate), gs, ptr(stats), ptr(dy),
-            ptr(dh), T, ptr(dx), ptr(db), ptr(dgate), dgs, g,
+            ctypes.byref(bn.c(cfg, where, dev)), _flat(where, "y", y, shape, io, dev),
+            _flat(where, "b", b, shape, io, dev), ptr(gate), gs,
+            _flat(where, "stats", stats, (T, 4), torch.float32, dev), _flat(where, "dy", dy, shape, io, dev),
+            _flat(where, "dh", dh, shape, io, dev), T, _flat(where, "dx", dx, shape, io, dev),
+            _flat(where, "db", db, shape, dt, dev), ptr(dgate), dgs, g,
             ws_bytes=0 if g is None else L.hstu_block_norm_bwd_workspace_size(ctypes.byref(cfg), T))
     return dx
 
@@ -695,31 +710,33 @@ def checkpoint_bytes(cfg: Config, fmt: int, T: int) -> int:
     return checkpoint_layout(cfg, T)[CKPT_COUNT]
 
 
-def _checkpoint_blocks(where, cfg, saved, ckpt, T, fmt):
-    dev = saved.device
-    for n, t, need in (("saved", saved, saved_layout(cfg, T)[SAVED_COUNT]),
-                       ("ckpt", ckpt, checkpoint_bytes(cfg, fmt, T))):
-        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous() or t.numel() < need:
+def _checkpoint_blocks(where, cfg, saved, ckpt, T):
+    L, c, dev = lib(), ctypes.byref(cfg), saved.device
+    saved_bytes, offsets = c_size_t(0), (c_size_t * (CKPT_COUNT + 1))()
+    _check(L.hstu_workspace_size(c, 0, T, None, ctypes.byref(saved_bytes)), "hstu_workspace_size")
+    _check(L.hstu_checkpoint_layout(c, T, offsets), "hstu_checkpoint_layout")
+    for n, t, need in (("saved", saved, saved_bytes.value), ("ckpt", ckpt, offsets[CKPT_COUNT])):
+        if t.dtype is not torch.uint8 or t.device != dev or not t.is_contiguous() or t.numel() < need:
             raise ValueError(f"{where}: {n} must be at least {need} contiguous bytes on {dev}")
     return dev
 
 
 def checkpoint_save(cfg: Config, fmt: int, saved, T: int, ckpt, stream=None):
     """Holds a layer's saved block (filled by fwd) in 8 bits (CKPT_INT8 or CKPT_E4M3); returns ckpt."""
-    dev = _checkpoint_blocks("checkpoint_save", cfg, saved, ckpt, T, fmt)
-    _launch("checkpoint_save", dev, stream, lib().hstu_checkpoint_save, ctypes.byref(cfg), fmt, ptr(saved), T,
-            ptr(ckpt))
+    dev = _checkpoint_blocks("checkpoint_save", cfg, saved, ckpt, T)
+    _launch("checkpoint_save", dev, stream, lib().hstu_checkpoint_save, ctypes.byref(cfg), fmt,
+            saved.data_ptr(), T, ckpt.data_ptr())
     return ckpt
 
 
 def checkpoint_restore(cfg: Config, fmt: int, ckpt, T: int, ln_gamma, ln_beta, saved, stream=None):
     """A saved block for bwd from a checkpoint and the layer's ln_gamma, ln_beta; returns saved."""
     where = "checkpoint_restore"
-    dev = _checkpoint_blocks(where, cfg, saved, ckpt, T, fmt)
-    for n, t in (("ln_gamma", ln_gamma), ("ln_beta", ln_beta)):
-        _flat(where, n, t, (cfg.d_model,), torch_dtype(cfg.dtype), dev)
-    _launch(where, dev, stream, lib().hstu_checkpoint_restore, ctypes.byref(cfg), fmt, ptr(ckpt), ptr(ln_gamma),
-            ptr(ln_beta), T, ptr(saved))
+    dev = _checkpoint_blocks(where, cfg, saved, ckpt, T)
+    shape, dt = (cfg.d_model,), torch_dtype(cfg.dtype)
+    _launch(where, dev, stream, lib().hstu_checkpoint_restore, ctypes.byref(cfg), fmt, ckpt.data_ptr(),
+            _flat(where, "ln_gamma", ln_gamma, shape, dt, dev),
+            _flat(where, "ln_beta", ln_beta, shape, dt, dev), T, saved.data_ptr())
     return saved
 
 
