@@ -3,8 +3,10 @@
 Moves a seeded workload to the GPU and runs it through the C ABI: a forward
 stack, a forward+backward training step, M-FALCON scoring (history pass
 with K/V caching, then candidate microbatches against the cache), and
-Stochastic Length sampling of a training batch.  Every layer step runs in
-libhstu.so.
+Stochastic Length sampling of a training batch.  Around the layers: an item
+embedding that feeds a training step and takes its gradient, activation
+checkpoints in 8 bits, and stacks with norms before and after each block.
+Every layer step runs in libhstu.so.
 """
 from __future__ import annotations
 
@@ -87,16 +89,101 @@ def forward_stack(dw: DeviceWorkload, num_layers: Optional[int] = None, stream=N
     return y
 
 
-class TrainStep:
-    """Buffers for a forward+backward step over the whole stack, allocated once."""
+class ItemEmbedding:
+    """An item table [V][dim] (fp32 or bf16 on the device), the scale of its lookups (default
+    sqrt(dim)) and its gradient: dense fp32 in `grad`, accumulated, or (rows=True, for tables
+    too large for that) the last batch's non-zero rows in `row_ids`, `rows` and `count`."""
 
-    def __init__(self, dw: DeviceWorkload, chain: bool = True):
+    def __init__(self, table: torch.Tensor, scale: Optional[float] = None, rows: bool = False):
+        self.table = table
+        self.scale = float(table.shape[1]) ** 0.5 if scale is None else float(scale)
+        self.grad = None if rows else torch.zeros(table.shape, dtype=torch.float32, device=table.device)
+        self.row_ids = self.rows = self.count = None
+
+    def lookup(self, ids, out, low=None, stream=None):
+        """out[t] = scale * table[ids[t]], zero for padding ids and for columns past dim."""
+        return H.embedding_fwd(self.table, ids, self.scale, out=out, low=low, stream=stream)
+
+    def backward(self, dx, ids, stream=None):
+        """Takes the gradient of lookup's out.  In the rows form the buffers of an earlier batch of
+        this size are written again."""
+        if self.grad is not None:
+            H.embedding_bwd(dx, ids, self.grad, self.scale, stream=stream)
+            return
+        V, dim = self.table.shape
+        cap = min(ids.shape[0], V)
+        if self.rows is None or self.rows.shape[0] != cap:
+            dev = self.table.device
+            self.row_ids = torch.zeros(cap, dtype=torch.int64, device=dev)
+            self.rows = torch.zeros(cap, dim, dtype=torch.float32, device=dev)
+            self.count = torch.zeros(1, dtype=torch.int64, device=dev)
+        H.embedding_bwd_rows(dx, ids, V, self.row_ids, self.rows, self.count, self.scale, stream=stream)
+
+    def zero_grad(self):
+        if self.grad is not None:
+            self.grad.zero_()
+
+
+CHECKPOINTS = {"int8": H.CKPT_INT8, "e4m3": H.CKPT_E4M3}
+
+
+class SavedBlocks:
+    """The saved blocks of a stack's layers, or (checkpoints "int8" or "e4m3") two blocks that the
+    layers take in turn and an 8-bit checkpoint of every layer but the last, whose backward is next."""
+
+    def __init__(self, dw: DeviceWorkload, checkpoints: Optional[str]):
+        if checkpoints is not None and checkpoints not in CHECKPOINTS:
+            raise ValueError(f"checkpoints must be one of {sorted(CHECKPOINTS)} or None, got {checkpoints!r}")
         self.dw = dw
-        T = dw.T
-        _, saved_n = H.workspace_size(dw.cfg, dw.B, T)
+        self.fmt = None if checkpoints is None else CHECKPOINTS[checkpoints]
+        L, dev = len(dw.layers), dw.x.device
+        n = H.saved_layout(dw.cfg, dw.T)[H.SAVED_COUNT]
+        blocks = [torch.empty(n, dtype=torch.uint8, device=dev)
+                  for _ in range(L if self.fmt is None else min(L, 2))]
+        self.blocks = [blocks[i % len(blocks)] for i in range(L)]
+        self.ckpt = []
+        if self.fmt is not None:
+            m = H.checkpoint_bytes(dw.cfg, self.fmt, dw.T)
+            self.ckpt = [torch.empty(m, dtype=torch.uint8, device=dev) for _ in range(L - 1)]
+
+    def after_forward(self, i, stream=None):
+        """Layer i's block has been filled."""
+        if i < len(self.ckpt):
+            H.checkpoint_save(self.dw.cfg, self.fmt, self.blocks[i], self.dw.T, self.ckpt[i], stream=stream)
+
+    def before_backward(self, i, stream=None):
+        """Layer i's block, as its backward reads it."""
+        if i < len(self.ckpt):
+            w = self.dw.layers[i]
+            H.checkpoint_restore(self.dw.cfg, self.fmt, self.ckpt[i], self.dw.T, w.ln_gamma, w.ln_beta,
+                                 self.blocks[i], stream=stream)
+        return self.blocks[i]
+
+
+class TrainStep:
+    """Buffers for a forward+backward step over the whole stack, allocated once.
+
+    checkpoints ("int8" or "e4m3"): hold the layers' saved activations in 8 bits between the
+    forward and the backward; with an fp32 residual stream and bf16 operands neither the blocks
+    nor the layers' inputs are then kept per layer (28d bytes a token and layer become 6.19d).
+    embedding and ids: the stack's rows are looked up in an item table at the start of every run,
+    and its gradient is taken at the end (dw.x is not used)."""
+
+    def __init__(self, dw: DeviceWorkload, chain: bool = True, checkpoints: Optional[str] = None,
+                 embedding: Optional[ItemEmbedding] = None, ids: Optional[torch.Tensor] = None):
+        if (embedding is None) != (ids is None):
+            raise ValueError("embedding and ids go together")
+        self.dw = dw
+        self.embedding, self.ids = embedding, ids
+        T, L = dw.T, len(dw.layers)
         dev = dw.x.device
-        self.saved = [torch.empty(saved_n, dtype=torch.uint8, device=dev) for _ in dw.layers]
-        self.acts = [dw.x] + [torch.empty_like(dw.x) for _ in dw.layers]
+        self.store = SavedBlocks(dw, checkpoints)
+        self.saved = self.store.blocks
+        x = dw.x if embedding is None else torch.empty_like(dw.x)
+        # the backward reads a layer's input only where the saved block has no operand copy of it
+        keep = checkpoints is None or dw.cfg.io_dtype == dw.cfg.dtype
+        bufs = [torch.empty_like(dw.x) for _ in range(L if keep else min(L, 2))]
+        self.acts = [x] + [bufs[i % len(bufs)] for i in range(L)]
         self.gbuf = [torch.empty_like(dw.x), torch.empty_like(dw.x)]
         # fp32 residual stream with bf16 operands: each layer's output epilogue
         # also writes the bf16 copy the next layer reads (forward: straight
@@ -146,26 +233,117 @@ class TrainStep:
         dw = self.dw
         L = len(dw.layers)
         ch = self.chain
+        emb = self.embedding
+        if emb is not None:
+            emb.lookup(self.ids, self.acts[0], low=self.xlow[0] if ch and L else None, stream=stream)
         for i, w in enumerate(dw.layers):
             H.fwd(dw.cfg, w, self.acts[i], dw.offsets, dw.timestamps, dw.num_targets,
                   y=self.acts[i + 1], saved=self.saved[i], stream=stream,
-                  x_low=self.xlow[i] if ch and i > 0 else None,
+                  x_low=self.xlow[i] if ch and (i > 0 or emb is not None) else None,
                   y_low=self.xlow[i + 1] if ch and i + 1 < L else None)
+            self.store.after_forward(i, stream=stream)
         g = dw.dy if dy is None else dy
         for i in range(L - 1, -1, -1):
             out = self.gbuf[i % 2]
-            H.bwd(dw.cfg, dw.layers[i], self.acts[i], g, self.saved[i], dw.offsets, dw.timestamps,
+            H.bwd(dw.cfg, dw.layers[i], self.acts[i], g, self.store.before_backward(i, stream=stream),
+                  dw.offsets, dw.timestamps,
                   dw.num_targets, dx=out, grads=self.grads[i], stream=stream,
                   dy_low=self.dlow[(i + 1) % 2] if ch and i < L - 1 else None,
                   dx_low=self.dlow[i % 2] if ch and i > 0 else None)
             if on_layer_grads is not None:
                 on_layer_grads(i)
             g = out
+        if emb is not None:
+            emb.backward(g, self.ids, stream=stream)
         return g
 
     @property
     def y(self):
         return self.acts[-1]
+
+
+class NormedTrainStep:
+    """Forward+backward of a stack whose blocks sit between norms: with f_i the layer without its
+    residual sum (projection, attention, LayerNorm (.) U, projection) and joint i = joints[i],
+
+        y_0 = x,  h_0 = Norm_pre(y_0);   b_i = f_i(h_i)
+        y_(i+1) = y_i + s (.) (Norm_post(b_i) (.) act(gates[i])),  h_(i+1) = Norm_pre(y_(i+1))
+
+    with Norm_pre of joint i before block i, and Norm_post, s and the gate's activation of joint
+    i + 1 after it (so joints has one more entry than the stack has layers, the first joint's
+    Norm_post and the last one's Norm_pre are not used).  gates: a [T][d] tensor (cfg->dtype) or
+    None for each block; their gradients are left in dgates.  checkpoints as in TrainStep."""
+
+    def __init__(self, dw: DeviceWorkload, joints: List[H.BlockNorm], gates=None,
+                 checkpoints: Optional[str] = None):
+        cfg, T, L, dev = dw.cfg, dw.T, len(dw.layers), dw.x.device
+        if len(joints) != L + 1:
+            raise ValueError(f"a stack of {L} layers has {L + 1} joints, got {len(joints)}")
+        self.dw, self.joints = dw, joints
+        self.gates = [None] * L if gates is None else list(gates)
+        dt = H.torch_dtype(cfg.dtype)
+        d = cfg.d_model
+        self.store = SavedBlocks(dw, checkpoints)
+        self.views = [H.saved_views(cfg, b, T) for b in self.store.blocks]
+        low = lambda: torch.empty(T, d, dtype=dt, device=dev)
+        # a block's operand h lives in its saved block where that holds one
+        self.h = [v["xlow"] if "xlow" in v else low() for v in self.views]
+        self.y_ = [dw.x] + [torch.empty_like(dw.x) for _ in range(L)]
+        self.b = [torch.empty_like(dw.x) for _ in range(L)]
+        self.stats = [torch.empty(T, 4, dtype=torch.float32, device=dev) for _ in range(L + 1)]
+        self.dgates = [None if g is None else torch.empty(T, d, dtype=dt, device=dev) for g in self.gates]
+        self.grads = [H.LayerGradBufs.zeros_like(w, dev) for w in dw.layers]
+        self.joint_grads = [H.BlockNormGrads.zeros_like(j) for j in joints]
+        self.db, self.dz, self.do = low(), low(), low()
+        self.dpre = torch.empty(T, 4 * d, dtype=dt, device=dev)
+        self.dh, self.dy = torch.empty_like(dw.x), torch.empty_like(dw.x)
+
+    def zero_grads(self):
+        for g in (*self.grads, *self.joint_grads):
+            for t in vars(g).values():
+                if t is not None:
+                    t.zero_()
+
+    @property
+    def y(self):
+        return self.y_[-1]
+
+    def run(self, dy=None, stream=None):
+        """Forward, then backward from dy; returns dX (a buffer of this step)."""
+        dw, cfg, st = self.dw, self.dw.cfg, {"stream": stream}
+        L = len(dw.layers)
+        H.block_norm_fwd(cfg, self.joints[0], self.y_[0], h=self.h[0] if L else None, stats=self.stats[0],
+                         want_h=L > 0, **st)
+        for i, w in enumerate(dw.layers):
+            v = self.views[i]
+            H.proj_in_fwd(cfg, w, self.h[i], v["pre"], v["g"], **st)
+            H.attention_fwd(cfg, w.rab_pos, w.rab_time, v["g"], dw.offsets, dw.timestamps, dw.num_targets,
+                            v["o"], **st)
+            H.ln_gate_fwd(cfg, w.ln_gamma, w.ln_beta, v["o"], v["g"], v["z"], v["mean"], v["rstd"], **st)
+            H.proj_out_fwd(cfg, w.W2, w.b2, v["z"], None, self.b[i], **st)
+            self.store.after_forward(i, **st)
+            last = i + 1 == L
+            H.block_norm_fwd(cfg, self.joints[i + 1], self.y_[i], self.b[i], self.gates[i], y=self.y_[i + 1],
+                             h=None if last else self.h[i + 1], stats=self.stats[i + 1], want_h=not last, **st)
+        g = dw.dy if dy is None else dy
+        dh = None
+        for i in range(L - 1, -1, -1):
+            w, gr, v = dw.layers[i], self.grads[i], self.views[i]
+            g = H.block_norm_bwd(cfg, self.joints[i + 1], self.y_[i + 1], self.b[i], self.gates[i],
+                                 self.stats[i + 1], dy=g, dh=dh, dx=self.dy, db=self.db, dgate=self.dgates[i],
+                                 grads=self.joint_grads[i + 1], **st)
+            self.store.before_backward(i, **st)
+            H.proj_out_bwd(cfg, w.W2, v["z"], self.db, self.dz, gr.dW2, gr.db2, **st)
+            H.ln_gate_bwd(cfg, w.ln_gamma, w.ln_beta, self.dz, v["o"], v["g"], v["pre"], v["mean"], v["rstd"],
+                          self.do, self.dpre, gr.dgamma, gr.dbeta, **st)
+            H.attention_bwd(cfg, w.rab_pos, w.rab_time, v["g"], v["pre"], self.do, dw.offsets, dw.timestamps,
+                            dw.num_targets, self.dpre, gr.drab_pos, gr.drab_time, **st)
+            H.proj_in_bwd(cfg, w.W1, self.h[i], self.dpre, None, self.dh, gr.dW1, gr.db1, **st)
+            dh = self.dh
+        if L == 0:
+            return g
+        return H.block_norm_bwd(cfg, self.joints[0], self.y_[0], None, None, self.stats[0], dy=g, dh=dh,
+                                dx=self.dy, grads=self.joint_grads[0], **st)
 
 
 def _gather(src, rows: np.ndarray, out=None):

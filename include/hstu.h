@@ -338,8 +338,9 @@ hstu_status hstu_fwd_cached(const hstu_config* cfg, const hstu_weights* w, const
                             const int64_t* hist_timestamps, void* y, void* workspace,
                             size_t ws_bytes, cudaStream_t stream);
 
-/* One layer backward.  x is the layer input of the forward, saved the block
- * the forward filled; dy [T][d] upstream; dx [T][d] output (may alias dy);
+/* One layer backward.  x is the layer input of the forward (read only when
+ * io_dtype equals dtype: the saved block holds its operand copy otherwise), saved
+ * the block the forward filled or hstu_checkpoint_restore gave back; dy [T][d] upstream; dx [T][d] output (may alias dy);
  * x, dy, dx in cfg->io_dtype.
  * Gradients accumulate into *grads (members may be NULL). */
 hstu_status hstu_bwd(const hstu_config* cfg, const hstu_weights* w, const void* x,
