@@ -627,23 +627,24 @@ struct GradPtrs {
 };
 
 // grads.p[i][c] += sum over the CTAs of partial[cta][i][c], in the order of
-// the CTAs within each of 8 strips, then of the strips.
-__global__ void __launch_bounds__(256) block_norm_join_kernel(const float* __restrict__ partial, int ctas, int d,
-                                                              GradPtrs grads) {
-  __shared__ float strip[8][32];
+// the CTAs within each of 32 strips, then of the strips.
+constexpr int kStrips = 32;
+__global__ void __launch_bounds__(32 * kStrips) block_norm_join_kernel(const float* __restrict__ partial, int ctas,
+                                                                       int d, GradPtrs grads) {
+  __shared__ float strip[kStrips][32];
   float* const out = grads.p[blockIdx.y];
   if (!out) return;
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   const float* src = partial + (int64_t)blockIdx.y * d + c;
   float t = 0.f;
   if (c < d)
-#pragma unroll 8
-    for (int i = w; i < ctas; i += 8) t += src[(int64_t)i * kParams * d];
-  strip[w][threadIdx.x % 32] = t;
+#pragma unroll 4
+    for (int i = w; i < ctas; i += kStrips) t += src[(int64_t)i * kParams * d];
+  strip[w][lane] = t;
   __syncthreads();
   if (w == 0 && c < d) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) t += strip[k][threadIdx.x];
+    for (int k = 1; k < kStrips; ++k) t += strip[k][lane];
     out[c] += t;
   }
 }
@@ -717,7 +718,7 @@ cudaError_t launch_bwd(const BwdArgs<T>& p, const void* y, const void* b, const 
   count_launch();
   e = cudaGetLastError();
   if (e == cudaSuccess && p.partial) {
-    block_norm_join_kernel<<<dim3((unsigned)((p.d + 31) / 32), kParams), 256, 0, s>>>(p.partial, ctas, p.d, grads);
+    block_norm_join_kernel<<<dim3((unsigned)((p.d + 31) / 32), kParams), 32 * kStrips, 0, s>>>(p.partial, ctas, p.d, grads);
     count_launch();
     e = cudaGetLastError();
   }

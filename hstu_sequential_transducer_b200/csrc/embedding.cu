@@ -138,11 +138,10 @@ struct PairSource {
   }
 };
 
-// A pass sorts by the digit (key >> shift) & mask.
+// A pass sorts by the digit of `width` bits from `shift` on.
 struct Pass {
-  int shift;
-  uint32_t mask;
-  __device__ __forceinline__ uint32_t digit(uint32_t key) const { return (key >> shift) & mask; }
+  int shift, width;
+  __device__ __forceinline__ uint32_t digit(uint32_t key) const { return (key >> shift) & ((1u << width) - 1u); }
 };
 
 // Counts the first pass's digits of every tile, and clears the counts of the
@@ -234,20 +233,33 @@ __device__ __forceinline__ void warps_first(uint32_t (*count)[kDigits], uint32_t
   }
 }
 
+// The lanes that have a pair of the same digit, by a vote for each of its bits
+// (a pass's launch takes 8.6 us with it, 10.1 with the instruction that matches whole values).
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int width, bool in) {
+  uint32_t peers = __ballot_sync(0xffffffffu, in);
+  for (int b = 0; b < width; ++b) {
+    const bool one = (digit >> b) & 1u;
+    const uint32_t ones = __ballot_sync(0xffffffffu, one);
+    peers &= one ? ones : ~ones;
+  }
+  return peers;
+}
+
 // Stable ranks of N pairs a thread: warps hold consecutive runs of 32 N pairs,
 // pair i of a lane the one 32 i + lane places on.  rank: the pair's place among
 // those of its digit in its warp; count[warp][digit]: how many the warp has.
 template <int N>
-__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[N], const bool (&in)[N], uint32_t (&rank)[N],
-                                           uint32_t* count) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[N], const bool (&in)[N], int width,
+                                           uint32_t (&rank)[N], uint32_t (&peers)[N], uint32_t* count) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) peers[i] = same_digit(digit[i], width, in[i]);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t peers = __match_any_sync(0xffffffffu, in[i] ? digit[i] : 0x10000u);
-    const uint32_t ahead = __popc(peers & ((1u << lane) - 1u));
+    const uint32_t ahead = __popc(peers[i] & below);
     const uint32_t seen = in[i] ? count[digit[i]] : 0u;
     __syncwarp();
-    if (in[i] && ahead == 0) count[digit[i]] = seen + __popc(peers);
+    if (in[i] && ahead == 0) count[digit[i]] = seen + __popc(peers[i]);
     __syncwarp();
     rank[i] = seen + ahead;
   }
@@ -271,7 +283,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const int64_t base = (int64_t)blockIdx.x * kTile + warp * (32 * N) + lane;
   uint2 pair[N];
-  uint32_t digit[N], rank[N];
+  uint32_t digit[N], rank[N], peers[N];
   bool in[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
   }
   clear_counts(count);
   const uint32_t run = block_prefix(all, warp_tot) + earlier;      // where the tile's events of this digit go
-  warp_ranks<N>(digit, in, rank, count[warp]);
+  warp_ranks<N>(digit, in, pass.width, rank, peers, count[warp]);
   __syncthreads();
   if (tid < kDigits) warps_first(count, run);
   __syncthreads();
@@ -334,9 +346,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
       at = to / kTile * kDigits + next.digit(pair[i].x);
     }
     if (next_hist) {
-      // once for the warp's pairs that share it (a popular item's all do)
-      const uint32_t peers = __match_any_sync(0xffffffffu, at);
-      if (in[i] && (peers & ((1u << lane) - 1u)) == 0) atomicAdd(next_hist + at, (uint32_t)__popc(peers));
+      // once for those of the pair's peers that share the first one's counter (a popular item's all do)
+      const int first = __ffs(peers[i]) - 1;
+      const uint32_t lead = __shfl_sync(0xffffffffu, at, first < 0 ? 0 : first);
+      const uint32_t with = __ballot_sync(0xffffffffu, in[i] && at == lead) & peers[i];
+      if (in[i] && (at != lead || lane == first)) atomicAdd(next_hist + at, at != lead ? 1u : (uint32_t)__popc(with));
     }
   }
 }
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src
   const int per = (T + kSortThreads - 1) / kSortThreads;
   const int base = warp * (32 * per) + lane;
   uint2 pair[N];
-  uint32_t digit[N], rank[N];
+  uint32_t digit[N], rank[N], peers[N];
   bool in[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -365,12 +379,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src
   }
   const int width = (bits + passes - 1) / passes;
   for (int p = 0; p < passes; ++p) {
-    const Pass pass{p * width, (1u << width) - 1u};
+    const Pass pass{p * width, width};
     clear_counts(count);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) digit[i] = pass.digit(pair[i].x);
-    warp_ranks<N>(digit, in, rank, count[warp]);
+    warp_ranks<N>(digit, in, width, rank, peers, count[warp]);
     __syncthreads();
     uint32_t all = 0;
     if (tid < kDigits)
@@ -795,7 +809,7 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
     e = cudaFuncSetAttribute(direct ? sort_scatter_kernel<true> : sort_scatter_kernel<false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    const auto pass = [&](int p) { return Pass{p * width, (1u << width) - 1u}; };
+    const auto pass = [&](int p) { return Pass{p * width, width}; };
     sort_hist_kernel<<<(unsigned)l.tiles, kSortThreads, 0, s>>>(src, T, pass(0), passes, hist, stride, joins);
     count_launch();
     for (int p = 0; p < passes; ++p) {
