@@ -355,11 +355,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
   }
 }
 
-// All passes of T <= kSmallSort events, in shared memory.
+// All passes of T <= kSmallSort events, in shared memory; with heads, also
+// what heads_kernel and supers_kernel leave for the rows form.
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src, int T, int bits, int passes,
                                                                   uint2* __restrict__ out,
-                                                                  uint32_t* __restrict__ joins) {
+                                                                  uint32_t* __restrict__ joins,
+                                                                  uint32_t* __restrict__ heads,
+                                                                  uint32_t* __restrict__ supers,
+                                                                  int64_t* __restrict__ num_rows) {
   constexpr int N = kSmallSort / kSortThreads;
+  static_assert(kSmallSort / kChunk <= kSortThreads, "a thread counts a chunk");
   extern __shared__ uint32_t dyn[];
   uint32_t(*const count)[kDigits] = reinterpret_cast<uint32_t(*)[kDigits]>(dyn);       // [kSortWarps]
   uint2* const buf = reinterpret_cast<uint2*>(dyn + kSortWarps * kDigits);              // [kSmallSort]
@@ -393,16 +398,35 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src
     const uint32_t run = block_prefix(all, warp_tot);
     if (tid < kDigits) warps_first(count, run);
     __syncthreads();
-    uint2* const to = p + 1 == passes ? out : buf;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (in[i]) to[count[warp][digit[i]] + rank[i]] = pair[i];
-    if (p + 1 == passes) return;
+      if (in[i]) buf[count[warp][digit[i]] + rank[i]] = pair[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (in[i]) pair[i] = buf[base + i * 32];
-    __syncthreads();
+    if (p + 1 < passes) __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (in[i]) out[base + i * 32] = pair[i];
+  if (!heads) return;
+  uint32_t n = 0;               // items that begin in this thread's chunk
+  const int chunks = (T + kChunk - 1) / kChunk;
+  if (tid < chunks) {
+    uint32_t left = tid > 0 ? buf[tid * kChunk - 1].x : src.V;
+    for (int t = tid * kChunk; t < min((tid + 1) * kChunk, T); ++t) {
+      const uint32_t k = buf[t].x;
+      n += k < src.V && k != left;
+      left = k;
+    }
+  }
+  __syncthreads();              // the last pass has read warp_tot
+  const uint32_t before = block_prefix(n, warp_tot);
+  if (tid < chunks) {
+    heads[tid] = before;
+    if (tid % (kSuper / kChunk) == 0) supers[tid / (kSuper / kChunk)] = 0;
+    if (tid == chunks - 1) *num_rows = before + n;
   }
 }
 
@@ -790,6 +814,8 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
   uint32_t* const hist = reinterpret_cast<uint32_t*>(base + l.hist);
   uint32_t* const totals = reinterpret_cast<uint32_t*>(base + l.totals);
   uint32_t* const joins = reinterpret_cast<uint32_t*>(base + l.joins);
+  uint32_t* const heads = reinterpret_cast<uint32_t*>(base + l.heads);
+  uint32_t* const supers = reinterpret_cast<uint32_t*>(base + l.supers);
   int bits = 0;
   while (((uint64_t)V >> bits) != 0) ++bits;                      // keys are 0 .. V
   const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes;
@@ -799,7 +825,8 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
     constexpr int kBytes = kSortWarps * kDigits * 4 + kSmallSort * 8;
     e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    sort_small_kernel<<<1, kSortThreads, kBytes, s>>>(src, (int)T, bits, passes, pairs[0], joins);
+    sort_small_kernel<<<1, kSortThreads, kBytes, s>>>(src, (int)T, bits, passes, pairs[0], joins,
+                                                      row_ids ? heads : nullptr, supers, num_rows);
     count_launch();
     src.pairs = pairs[0];
   } else {
@@ -840,20 +867,20 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
   a.scale = scale;
   a.dst = dst;
   a.dst_stride = dst_stride;
-  a.heads = reinterpret_cast<uint32_t*>(base + l.heads);
-  a.supers = reinterpret_cast<uint32_t*>(base + l.supers);
+  a.heads = heads;
+  a.supers = supers;
   a.row_ids = row_ids;
   a.partial = reinterpret_cast<float*>(base + l.partial);
   a.joins = joins;
   if (!row_ids)
     return dout_dtype == HSTU_BF16 ? launch_sum<bf16, false>(a, dout, s) : launch_sum<float, false>(a, dout, s);
-  heads_kernel<<<(unsigned)l.nsupers, kSuper, 0, s>>>(src.pairs, T, (uint32_t)V, l.chunks,
-                                                      reinterpret_cast<uint32_t*>(base + l.heads),
-                                                      reinterpret_cast<uint32_t*>(base + l.supers));
-  supers_kernel<<<1, 1024, 0, s>>>(reinterpret_cast<uint32_t*>(base + l.supers), l.nsupers, num_rows);
-  count_launch(2);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (T > kSmallSort) {
+    heads_kernel<<<(unsigned)l.nsupers, kSuper, 0, s>>>(src.pairs, T, (uint32_t)V, l.chunks, heads, supers);
+    supers_kernel<<<1, 1024, 0, s>>>(supers, l.nsupers, num_rows);
+    count_launch(2);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   return dout_dtype == HSTU_BF16 ? launch_sum<bf16, true>(a, dout, s) : launch_sum<float, true>(a, dout, s);
 }
 
