@@ -22,6 +22,7 @@
 #include "args.h"
 #include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace hstu {
 namespace {
@@ -39,8 +40,11 @@ constexpr int kAlone = 32;           // an item that goes on for more chunks is 
 // (2 KB of each: 1.5 us for 71 tiles, 5 for 192); above, a kernel of its own
 // scans them once for all CTAs (4 us with its launch).
 constexpr int kDirectTiles = 128;
-// Up to this many events are sorted by one CTA in one launch.
+// Up to this many events are sorted by one CTA in one launch, and up to eight
+// times as many by a cluster of CTAs, also in one launch (14,001 events in two
+// passes: 14 us; as a launch for the counts and one for each pass 21).
 constexpr int kSmallSort = 4096;
+constexpr int kSortCluster = 8;
 
 // N consecutive elements in one access of N * sizeof(T) bytes.
 template <int BYTES> struct Raw;
@@ -352,6 +356,74 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
       const uint32_t with = __ballot_sync(0xffffffffu, in[i] && at == lead) & peers[i];
       if (in[i] && (at != lead || lane == first)) atomicAdd(next_hist + at, at != lead ? 1u : (uint32_t)__popc(with));
     }
+  }
+}
+
+// The word at the same place of shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::cluster_addr(p, rank)) : "memory");
+  return v;
+}
+
+// All passes of a cluster's CTAs, a tile each: they read one another's counts
+// from shared memory, and pass on the pairs through the buffers a and b (L2).
+__global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(PairSource src, int T, int bits, int passes,
+                                                                    uint2* a, uint2* b,
+                                                                    uint32_t* __restrict__ joins) {
+  constexpr int N = kTile / kSortThreads;
+  extern __shared__ uint32_t dyn[];
+  uint32_t(*const count)[kDigits] = reinterpret_cast<uint32_t(*)[kDigits]>(dyn);       // [kSortWarps]
+  __shared__ uint32_t tile_count[kDigits];
+  __shared__ uint32_t warp_tot[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const uint32_t rank_of_cta = tc::cluster_rank();
+  if (blockIdx.x == 0 && tid < 2) joins[tid] = 0;
+  const int base = (int)blockIdx.x * kTile + warp * (32 * N) + lane;
+  const int width = (bits + passes - 1) / passes;
+  uint2 pair[N];
+  uint32_t digit[N], rank[N], peers[N];
+  bool in[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    in[i] = base + i * 32 < T;
+    pair[i] = in[i] ? src(base + i * 32) : make_uint2(0, 0);
+  }
+  for (int p = 0; p < passes; ++p) {
+    const Pass pass{p * width, width};
+    uint2* const to = p & 1 ? b : a;
+    clear_counts(count);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) digit[i] = pass.digit(pair[i].x);
+    warp_ranks<N>(digit, in, width, rank, peers, count[warp]);
+    __syncthreads();
+    if (tid < kDigits) {
+      uint32_t n = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) n += count[w][tid];
+      tile_count[tid] = n;
+    }
+    tc::cluster_sync();
+    uint32_t all = 0, earlier = 0;
+    if (tid < kDigits)
+      for (uint32_t r = 0; r < gridDim.x; ++r) {
+        const uint32_t n = cluster_load(tile_count + tid, r);
+        all += n;
+        earlier += r < rank_of_cta ? n : 0u;
+      }
+    const uint32_t run = block_prefix(all, warp_tot) + earlier;
+    if (tid < kDigits) warps_first(count, run);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (in[i]) to[count[warp][digit[i]] + rank[i]] = pair[i];
+    // the counts have been read and the pairs are written, by every CTA
+    tc::cluster_sync();
+    if (p + 1 < passes)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (in[i]) pair[i] = __ldcg(to + base + i * 32);
   }
 }
 
@@ -829,6 +901,25 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
                                                       row_ids ? heads : nullptr, supers, num_rows);
     count_launch();
     src.pairs = pairs[0];
+  } else if (l.tiles <= kSortCluster) {
+    constexpr int kBytes = kSortWarps * kDigits * 4;
+    e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)l.tiles;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)l.tiles);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, sort_cluster_kernel, src, (int)T, bits, passes, pairs[0], pairs[1], joins);
+    count_launch();
+    if (e != cudaSuccess) return e;
+    src.pairs = pairs[(passes - 1) & 1];
   } else {
     const int64_t stride = l.tiles * kDigits;
     constexpr int kBytes = kSortWarps * kDigits * 4;

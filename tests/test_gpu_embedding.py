@@ -88,7 +88,7 @@ def check_grad(dout, ids, V, dim, scale, prior, got):
 
 
 CASES = [(1, 64, 1), (31, 50, 10), (32, 8, 2), (33, 1, 1), (64, 128, 1), (1000, 50, 3706), (2049, 96, 300), (5000, 33, 70_000),
-         (9000, 256, 17), (4096, 64, 16_777_217), (4097, 48, 513), (20_000, 512, 3), (600_001, 3, 777)]
+         (9000, 256, 17), (4096, 64, 16_777_217), (4097, 48, 513), (8200, 16, 1 << 28), (20_000, 512, 3), (32_768, 8, 4000), (32_769, 8, 4000), (600_001, 3, 777)]
 
 
 @pytest.mark.parametrize("T,dim,V", [c for c in CASES if c[1] * c[2] <= 1 << 28])
