@@ -12,8 +12,8 @@
 //
 // Memory-bound (a token reads 10d bytes and writes 6d in the forward, reads
 // 16d and writes 8d in the backward, with bf16 operands and an fp32 residual
-// stream).  A team of TPR threads, 8 columns a thread, takes R rows at a time: 4 in
-// the forward, 2 in the backward.  The columns stay the same, so the
+// stream).  A team of TPR threads, 8 columns a thread (a power of two below a
+// warp, else whole warps), takes R rows at a time: 4 in the forward, 1 or 2 in the backward.  The columns stay the same, so the
 // parameters are read once and the gradients' sums stay in registers; the R
 // rows give the four sums that are joined together (4 means; 2 sums of 2
 // rows), at half the shuffles of four separate ones and one barrier.  The next
@@ -25,6 +25,7 @@
 // Measured at 131,072 x 1,024, bf16 operands, fp32 residual stream: forward
 // 340 us (6.3 TB/s; 372 with 4 resident CTAs, which takes registers from
 // each), backward 546 us (6.4 TB/s; 599 with 3 CTAs; 566 with one row at a time and 4).
+// With a bf16 residual stream (half the bytes, the same instructions) 0.7 of the copy rate.
 #include "args.h"
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -34,12 +35,17 @@ namespace hstu {
 namespace {
 
 constexpr int kParams = 5;      // post_gamma, post_beta, res_scale, pre_gamma, pre_beta
-constexpr int kFwdRows = 4, kBwdRows = 2;                // rows that a team takes at a time
-// Threads of a CTA, and the CTAs of a multiprocessor (of 128 threads).
-template <int TPR> constexpr int kThreads = TPR > 128 ? TPR : 128;
-constexpr int kFwdResident = 3, kBwdResident = 2;
-template <int TPR> constexpr int kFwdCtas = TPR > 128 ? kFwdResident / 2 : kFwdResident;
-template <int TPR> constexpr int kBwdCtas = TPR > 128 ? kBwdResident / 2 : kBwdResident;
+constexpr int kFwdRows = 4;     // rows that a team takes at a time in the forward
+// Threads of a CTA: one team of 96 or more, else as many teams as 128 threads are.
+template <int TPR> constexpr int kThreads = TPR >= 96 ? TPR : 128;
+// The backward takes two rows at a time with 8 warps on a multiprocessor, whose
+// registers then hold them; teams of 3, 5, 6 or 7 warps do not make 8, and take
+// one row at a time with up to 16 warps (d = 1,536: 312 us instead of 348 with one
+// team; d = 2,048 the other way round, 299 instead of 321).
+constexpr int bwd_rows(int team) { return team == 96 || (team > 128 && team < 256) ? 1 : 2; }
+// CTAs of a multiprocessor.
+constexpr int fwd_resident(int threads) { return threads > 192 ? 2 : 384 / threads; }
+constexpr int bwd_resident(int threads) { return bwd_rows(threads) == 1 ? 512 / threads : 256 / threads; }
 
 // Copies B (16 or 8) bytes from src, or zeros where `any` is false.
 template <int B> __device__ __forceinline__ void copy_async(void* dst, const void* src, bool any) {
@@ -155,7 +161,7 @@ template <int TPR> struct Team {
   // slot: the team's 2 x kWarps x 4 floats; flip alternates, so that a slot
   // is rewritten only after a barrier that follows its last read.
   template <int N> static __device__ __forceinline__ void join(float (&v)[N], float (*slot)[4], int& flip, int team) {
-    constexpr int L = TPR < 32 ? TPR : 32, G = L / N;        // lanes that share a sum
+    constexpr int L = TPR < 32 ? TPR : 32, G = L / N;        // lanes that share a sum, at least 1
     const int lane = threadIdx.x & 31;
     float t = v[0];
     if constexpr (N == 4) {
@@ -228,7 +234,7 @@ constexpr int kBwdSlots = 8 * (4 * (int)sizeof(IO) + (int)sizeof(T)) * kThreads<
 
 // T: operand type; IO: residual stream's type.
 template <typename T, typename IO, int TPR>
-__global__ void __launch_bounds__(kThreads<TPR>, kFwdCtas<TPR>) block_norm_fwd_kernel(FwdArgs<T> p, const IO* x,
+__global__ void __launch_bounds__(kThreads<TPR>, fwd_resident(kThreads<TPR>)) block_norm_fwd_kernel(FwdArgs<T> p, const IO* x,
                                                                                 const IO* __restrict__ b, IO* y) {
   using W = Team<TPR>;
   constexpr int NT = kThreads<TPR>, R = kFwdRows, kRow = kFwdSlots<T, IO, TPR>;
@@ -410,11 +416,11 @@ struct BwdArgs {
 };
 
 template <typename T, typename IO, int TPR>
-__global__ void __launch_bounds__(kThreads<TPR>, kBwdCtas<TPR>) block_norm_bwd_kernel(
+__global__ void __launch_bounds__(kThreads<TPR>, bwd_resident(kThreads<TPR>)) block_norm_bwd_kernel(
     BwdArgs<T> p, const IO* __restrict__ y, const IO* __restrict__ b, const IO* dy, const IO* __restrict__ dh,
     IO* dx) {
   using W = Team<TPR>;
-  constexpr int NT = kThreads<TPR>, R = kBwdRows, kRow = kBwdSlots<T, IO, TPR>;
+  constexpr int NT = kThreads<TPR>, R = bwd_rows(TPR), kRow = kBwdSlots<T, IO, TPR>;
   extern __shared__ __align__(16) unsigned char ring[];
   // row i's slots of dy, dh, y and b (array 0 .. 3) and of u
   auto at = [&](int i, int array) { return reinterpret_cast<IO*>(ring + i * kRow) + array * 8 * NT; };
@@ -649,22 +655,22 @@ __global__ void __launch_bounds__(32 * kStrips) block_norm_join_kernel(const flo
   }
 }
 
-// Threads of a team: the smallest power of two with 8 columns each.
+// Threads of a team, 8 columns each: a power of two below a warp, else warps.
 int team_threads(int d) {
-  int t = 8;
+  if (d > 256) return (d + 255) / 256 * 32;
+  int t = 4;
   while (8 * t < d) t *= 2;
   return t;
 }
 
 // CTAs that have rows, at most those that are resident (the backward's workspace
 // holds a partial sum of each).
-int64_t ctas_of(int d, int64_t T, int rows, int resident) {
-  const int threads = team_threads(d), teams = threads > 128 ? 1 : 128 / threads;
-  const int64_t want = (T + teams * rows - 1) / (teams * rows);
-  const int64_t cap = (int64_t)sm_count() * (threads > 128 ? resident / 2 : resident);
+int64_t ctas_of(int d, int64_t T, int rows, int (*resident)(int)) {
+  const int team = team_threads(d), threads = team >= 96 ? team : 128, teams = threads / team;
+  const int64_t want = (T + teams * rows - 1) / (teams * rows), cap = (int64_t)sm_count() * resident(threads);
   return want < cap ? want : cap;
 }
-int64_t bwd_ctas(int d, int64_t T) { return ctas_of(d, T, kBwdRows, kBwdResident); }
+int64_t bwd_ctas(int d, int64_t T) { return ctas_of(d, T, bwd_rows(team_threads(d)), bwd_resident); }
 
 // 48 KB, the kernel's static arrays included, need no permission.
 template <typename K> cudaError_t allow_shared(K* kernel, int bytes) {
@@ -677,7 +683,7 @@ cudaError_t launch_fwd(const FwdArgs<T>& p, const void* x, const void* b, void* 
   constexpr int kBytes = kFwdRows * kFwdSlots<T, IO, TPR>;
   cudaError_t e = allow_shared(block_norm_fwd_kernel<T, IO, TPR>, kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = ctas_of(p.d, p.rows, kFwdRows, kFwdResident);
+  const int64_t ctas = ctas_of(p.d, p.rows, kFwdRows, fwd_resident);
   block_norm_fwd_kernel<T, IO, TPR><<<(unsigned)ctas, kThreads<TPR>, kBytes, s>>>(
       p, static_cast<const IO*>(x), static_cast<const IO*>(b), static_cast<IO*>(y));
   count_launch();
@@ -696,11 +702,16 @@ cudaError_t run_fwd(const hstu_config* c, const hstu_block_norm* n, const void* 
   p.gate = b ? static_cast<const T*>(gate) : nullptr; p.gate_stride = gate_stride; p.rows = T_;
   p.h = static_cast<T*>(h); p.stats = reinterpret_cast<float4*>(stats);
   switch (team_threads(p.d)) {
+    case 4: return launch_fwd<T, IO, 4>(p, x, b, y, s);
     case 8: return launch_fwd<T, IO, 8>(p, x, b, y, s);
     case 16: return launch_fwd<T, IO, 16>(p, x, b, y, s);
     case 32: return launch_fwd<T, IO, 32>(p, x, b, y, s);
     case 64: return launch_fwd<T, IO, 64>(p, x, b, y, s);
+    case 96: return launch_fwd<T, IO, 96>(p, x, b, y, s);
     case 128: return launch_fwd<T, IO, 128>(p, x, b, y, s);
+    case 160: return launch_fwd<T, IO, 160>(p, x, b, y, s);
+    case 192: return launch_fwd<T, IO, 192>(p, x, b, y, s);
+    case 224: return launch_fwd<T, IO, 224>(p, x, b, y, s);
     default: return launch_fwd<T, IO, 256>(p, x, b, y, s);
   }
 }
@@ -708,7 +719,7 @@ cudaError_t run_fwd(const hstu_config* c, const hstu_block_norm* n, const void* 
 template <typename T, typename IO, int TPR>
 cudaError_t launch_bwd(const BwdArgs<T>& p, const void* y, const void* b, const void* dy, const void* dh,
                        void* dx, const GradPtrs& grads, cudaStream_t s) {
-  constexpr int kBytes = kBwdRows * kBwdSlots<T, IO, TPR>;
+  constexpr int kBytes = bwd_rows(TPR) * kBwdSlots<T, IO, TPR>;
   cudaError_t e = allow_shared(block_norm_bwd_kernel<T, IO, TPR>, kBytes);
   if (e != cudaSuccess) return e;
   const int ctas = (int)bwd_ctas(p.d, p.rows);
@@ -739,11 +750,16 @@ cudaError_t run_bwd(const hstu_config* c, const hstu_block_norm* n, const void* 
   p.db = static_cast<T*>(db); p.dgate = static_cast<T*>(dgate); p.dgate_stride = dgate_stride;
   p.partial = partial;
   switch (team_threads(p.d)) {
+    case 4: return launch_bwd<T, IO, 4>(p, y, b, dy, dh, dx, grads, s);
     case 8: return launch_bwd<T, IO, 8>(p, y, b, dy, dh, dx, grads, s);
     case 16: return launch_bwd<T, IO, 16>(p, y, b, dy, dh, dx, grads, s);
     case 32: return launch_bwd<T, IO, 32>(p, y, b, dy, dh, dx, grads, s);
     case 64: return launch_bwd<T, IO, 64>(p, y, b, dy, dh, dx, grads, s);
+    case 96: return launch_bwd<T, IO, 96>(p, y, b, dy, dh, dx, grads, s);
     case 128: return launch_bwd<T, IO, 128>(p, y, b, dy, dh, dx, grads, s);
+    case 160: return launch_bwd<T, IO, 160>(p, y, b, dy, dh, dx, grads, s);
+    case 192: return launch_bwd<T, IO, 192>(p, y, b, dy, dh, dx, grads, s);
+    case 224: return launch_bwd<T, IO, 224>(p, y, b, dy, dh, dx, grads, s);
     default: return launch_bwd<T, IO, 256>(p, y, b, dy, dh, dx, grads, s);
   }
 }

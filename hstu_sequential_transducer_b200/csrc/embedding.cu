@@ -979,7 +979,9 @@ template <typename TT, typename TO, bool LOW>
 cudaError_t launch_lookup(const void* table, int64_t V, int dim, int64_t table_stride, const void* ids,
                           int id_bytes, int64_t T, float scale, void* out, int width, int64_t out_stride,
                           void* low, int64_t low_stride, cudaStream_t s) {
-  int n = 4;
+  // 16 bytes of the widest side, if alignment and widths allow
+  constexpr int kMost = sizeof(TT) == 2 && sizeof(TO) == 2 ? 8 : 4;
+  int n = kMost;
   while (n > 1 && !(vec_ok(n, table, sizeof(TT), table_stride, dim, width) &&
                     vec_ok(n, out, sizeof(TO), out_stride, dim, width) &&
                     (!LOW || vec_ok(n, low, 2, low_stride, dim, width))))
@@ -990,9 +992,14 @@ cudaError_t launch_lookup(const void* table, int64_t V, int dim, int64_t table_s
   const TT* t = static_cast<const TT*>(table);
   TO* o = static_cast<TO*>(out);
   bf16* l = static_cast<bf16*>(low);
-  if (n == 4) lookup_kernel<TT, TO, 4, LOW><<<grid, 256, 0, s>>>(t, V, dim, table_stride, ids, id_bytes, T, scale, o, width, out_stride, l, low_stride);
-  else if (n == 2) lookup_kernel<TT, TO, 2, LOW><<<grid, 256, 0, s>>>(t, V, dim, table_stride, ids, id_bytes, T, scale, o, width, out_stride, l, low_stride);
-  else lookup_kernel<TT, TO, 1, LOW><<<grid, 256, 0, s>>>(t, V, dim, table_stride, ids, id_bytes, T, scale, o, width, out_stride, l, low_stride);
+#define HSTU_LAUNCH(N)                                                                                          \
+  lookup_kernel<TT, TO, N, LOW><<<grid, 256, 0, s>>>(t, V, dim, table_stride, ids, id_bytes, T, scale, o, width, \
+                                                     out_stride, l, low_stride)
+  if (n == kMost) HSTU_LAUNCH(kMost);
+  else if (n == 4) HSTU_LAUNCH(4);
+  else if (n == 2) HSTU_LAUNCH(2);
+  else HSTU_LAUNCH(1);
+#undef HSTU_LAUNCH
   count_launch();
   return cudaGetLastError();
 }
