@@ -37,9 +37,10 @@ constexpr int kDigits = 512;         // of a pass, at most
 constexpr int kMaxPasses = 4;
 constexpr int kAlone = 32;           // an item that goes on for more chunks is a long one
 // Up to this many tiles, a CTA of the sort adds up the tiles' counts by itself
-// (2 KB of each: 1.5 us for 71 tiles, 5 for 192); above, a kernel of its own
-// scans them once for all CTAs (4 us with its launch).
-constexpr int kDirectTiles = 128;
+// (2 KB of each); above, a kernel of its own scans them once for all CTAs (two
+// launches more; whole gradients of 8 columns: 287,928 events 52.7 us by itself, 54.2
+// scanned; 400,000 65.0 and 64.6; 1,048,576 140.8 and 124.7).
+constexpr int kDirectTiles = 96;
 // Up to this many events are sorted by one CTA in one launch, and up to eight
 // times as many by a cluster of CTAs, also in one launch (14,001 events in two
 // passes: 14 us; as a launch for the counts and one for each pass 21).
@@ -121,6 +122,38 @@ __global__ void __launch_bounds__(256) lookup_kernel(const TT* __restrict__ tabl
 #pragma unroll
       for (int k = 0; k < N; ++k) l.v[k] = from_f<bf16>(f[k]);
       l.store(low + row[i] * low_stride + col[i]);
+    }
+  }
+}
+
+// Rows that allow no wider access than an element: a warp a row, kLookups * 2
+// of a lane's columns in flight.
+constexpr int kRowFlight = 2 * kLookups;
+template <typename TT, typename TO, bool LOW>
+__global__ void __launch_bounds__(256) lookup_rows_kernel(const TT* __restrict__ table, int64_t V, int dim,
+                                                          int64_t table_stride, const void* __restrict__ ids,
+                                                          int id_bytes, int64_t rows, float scale,
+                                                          TO* __restrict__ out, int width, int64_t out_stride,
+                                                          bf16* __restrict__ low, int64_t low_stride) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (row >= rows) return;
+  const int64_t id = id_at(ids, id_bytes, row);
+  const int have = id >= 0 && id < V ? dim : 0;
+  const TT* const src = table + (have ? id : 0) * table_stride;
+  out += row * out_stride;
+  if (LOW) low += row * low_stride;
+  for (int c0 = lane; c0 < width; c0 += 32 * kRowFlight) {
+    float f[kRowFlight];
+#pragma unroll
+    for (int i = 0; i < kRowFlight; ++i) f[i] = c0 + 32 * i < have ? to_f(src[c0 + 32 * i]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kRowFlight; ++i) {
+      const int c = c0 + 32 * i;
+      if (c >= width) break;
+      const float v = c < have ? scale * f[i] : 0.f;
+      out[c] = from_f<TO>(v);
+      if (LOW) low[c] = from_f<bf16>(v);
     }
   }
 }
@@ -975,6 +1008,10 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
   return dout_dtype == HSTU_BF16 ? launch_sum<bf16, true>(a, dout, s) : launch_sum<float, true>(a, dout, s);
 }
 
+// Rows that allow no wider access go to lookup_rows_kernel from this width on (67
+// million elements, fp32 with the bf16 copy: width 33 178 us by pieces, 297 by rows; 65
+// 174 and 173; 101 172 and 125; 333 168 and 94).
+constexpr int kRowsFrom = 64;
 template <typename TT, typename TO, bool LOW>
 cudaError_t launch_lookup(const void* table, int64_t V, int dim, int64_t table_stride, const void* ids,
                           int id_bytes, int64_t T, float scale, void* out, int width, int64_t out_stride,
@@ -986,12 +1023,19 @@ cudaError_t launch_lookup(const void* table, int64_t V, int dim, int64_t table_s
                     vec_ok(n, out, sizeof(TO), out_stride, dim, width) &&
                     (!LOW || vec_ok(n, low, 2, low_stride, dim, width))))
     n >>= 1;
-  const int64_t ctas = (T * (width / n) + 256 * kLookups - 1) / (256 * kLookups);
+  const bool by_rows = n == 1 && width >= kRowsFrom;
+  const int64_t ctas = by_rows ? (T + 7) / 8 : (T * (width / n) + 256 * kLookups - 1) / (256 * kLookups);
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)ctas;
   const TT* t = static_cast<const TT*>(table);
   TO* o = static_cast<TO*>(out);
   bf16* l = static_cast<bf16*>(low);
+  if (by_rows) {
+    lookup_rows_kernel<TT, TO, LOW><<<grid, 256, 0, s>>>(t, V, dim, table_stride, ids, id_bytes, T, scale, o, width,
+                                                         out_stride, l, low_stride);
+    count_launch();
+    return cudaGetLastError();
+  }
 #define HSTU_LAUNCH(N)                                                                                          \
   lookup_kernel<TT, TO, N, LOW><<<grid, 256, 0, s>>>(t, V, dim, table_stride, ids, id_bytes, T, scale, o, width, \
                                                      out_stride, l, low_stride)

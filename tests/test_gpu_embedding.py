@@ -43,7 +43,7 @@ def f64(t):
 @pytest.mark.parametrize("table_t,out_t,low", [("f32", "f32", True), ("bf16", "f32", True), ("f32", "f32", False),
                                                ("f32", "bf16", False), ("bf16", "bf16", False)])
 @pytest.mark.parametrize("T,dim,width,V,pad", [(1, 64, 64, 1, 0), (7, 50, 64, 3706, 0), (513, 33, 41, 97, 3), (100, 1, 1, 5, 0),
-                                               (64, 512, 512, 1000, 8), (1000, 1024, 1024, 300, 0), (3, 2050, 2050, 9, 2)])
+                                               (64, 512, 512, 1000, 8), (1000, 1024, 1024, 300, 0), (3, 2050, 2050, 9, 2), (90, 77, 333, 50, 2)])
 def test_lookup(table_t, out_t, low, T, dim, width, V, pad):
     rng = np.random.default_rng(T * 7 + dim)
     ty = {"f32": torch.float32, "bf16": torch.bfloat16}
