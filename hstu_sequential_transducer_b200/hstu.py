@@ -8,6 +8,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from dataclasses import dataclass
@@ -710,12 +711,19 @@ def checkpoint_bytes(cfg: Config, fmt: int, T: int) -> int:
     return checkpoint_layout(cfg, T)[CKPT_COUNT]
 
 
+@functools.lru_cache(maxsize=256)
+def _checkpoint_sizes(fields, T: int):
+    """Bytes of a saved block and of its checkpoint for a config of these fields."""
+    cfg = Config(*fields)
+    return saved_layout(cfg, T)[SAVED_COUNT], checkpoint_layout(cfg, T)[CKPT_COUNT]
+
+
 def _checkpoint_blocks(where, cfg, saved, ckpt, T):
-    L, c, dev = lib(), ctypes.byref(cfg), saved.device
-    saved_bytes, offsets = c_size_t(0), (c_size_t * (CKPT_COUNT + 1))()
-    _check(L.hstu_workspace_size(c, 0, T, None, ctypes.byref(saved_bytes)), "hstu_workspace_size")
-    _check(L.hstu_checkpoint_layout(c, T, offsets), "hstu_checkpoint_layout")
-    for n, t, need in (("saved", saved, saved_bytes.value), ("ckpt", ckpt, offsets[CKPT_COUNT])):
+    dev = saved.device
+    # the sizes depend on these fields; the others are only checked to be valid
+    sizes = _checkpoint_sizes((cfg.d_model, cfg.num_heads, cfg.head_dim, 1, 1, 1, 1.0, 0.0, cfg.dtype,
+                               cfg.io_dtype), T)
+    for n, t, need in (("saved", saved, sizes[0]), ("ckpt", ckpt, sizes[1])):
         if t.dtype is not torch.uint8 or t.device != dev or not t.is_contiguous() or t.numel() < need:
             raise ValueError(f"{where}: {n} must be at least {need} contiguous bytes on {dev}")
     return dev
