@@ -10,7 +10,7 @@
 //
 // Memory-bound: the save reads 14d bytes a token and writes 6.19d (bf16
 // operands, fp32 residual stream), the restore reads 6.19d and writes 24d; the
-// arithmetic is some 12 instructions a value, most of them on pairs.  So the kernels are
+// arithmetic is 12 and 17 instructions a value, most of them on pairs.  So the kernels are
 // plain streams: many small CTAs, each in one part of the block; a thread
 // loads its pieces of 16 bytes (of the wider side) before it works on the first,
 // and neighbouring threads hold neighbouring pieces, so that every access covers
