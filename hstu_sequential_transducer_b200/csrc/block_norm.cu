@@ -403,6 +403,10 @@ __global__ void __launch_bounds__(kThreads<TPR>, fwd_resident(kThreads<TPR>)) bl
   }
 }
 
+struct GradPtrs {
+  float* p[kParams];
+};
+
 template <typename T>
 struct BwdArgs {
   int post, pre, act, d;
@@ -412,7 +416,8 @@ struct BwdArgs {
   const float4* stats;
   T *db, *dgate;
   int64_t dgate_stride;
-  float* partial;               // [gridDim.x][5][d], or NULL
+  float* partial;               // [gridDim.x][5][d]; NULL: not wanted, or one CTA
+  GradPtrs grads;               // where a single CTA adds its sums
 };
 
 template <typename T, typename IO, int TPR>
@@ -605,17 +610,17 @@ __global__ void __launch_bounds__(kThreads<TPR>, bwd_resident(kThreads<TPR>)) bl
         if (full || r0 + i < p.rows) cols.store(p.db + (r0 + i) * d, e[i]);
       }
   }
-  if (!p.partial) return;
-  float* const out = p.partial + (int64_t)blockIdx.x * kParams * d;
-  if (W::kTeams == 1) {
+  if (W::kTeams == 1 && p.partial) {
 #pragma unroll
-    for (int i = 0; i < kParams; ++i) cols.store(out + i * d, acc[i]);
+    for (int i = 0; i < kParams; ++i) cols.store(p.partial + ((int64_t)blockIdx.x * kParams + i) * d, acc[i]);
     return;
   }
   // joins the teams' sums in the ring, whose last copies hold nothing
   copy_wait<0>();
   float* const all = reinterpret_cast<float*>(ring);          // [kTeams][8 TPR]
   for (int i = 0; i < kParams; ++i) {
+    float* const add_to = p.partial ? nullptr : p.grads.p[i];
+    if (!p.partial && !add_to) continue;
     __syncthreads();
     cols.store(all + team * 8 * TPR, acc[i]);
     __syncthreads();
@@ -623,14 +628,11 @@ __global__ void __launch_bounds__(kThreads<TPR>, bwd_resident(kThreads<TPR>)) bl
       float t = 0.f;
 #pragma unroll
       for (int w = 0; w < W::kTeams; ++w) t += all[w * 8 * TPR + c];
-      out[i * d + c] = t;
+      if (p.partial) p.partial[((int64_t)blockIdx.x * kParams + i) * d + c] = t;
+      else add_to[c] += t;
     }
   }
 }
-
-struct GradPtrs {
-  float* p[kParams];
-};
 
 // grads.p[i][c] += sum over the CTAs of partial[cta][i][c], in the order of
 // the CTAs within each of 32 strips, then of the strips.
@@ -670,7 +672,14 @@ int64_t ctas_of(int d, int64_t T, int rows, int (*resident)(int)) {
   const int64_t want = (T + teams * rows - 1) / (teams * rows), cap = (int64_t)sm_count() * resident(threads);
   return want < cap ? want : cap;
 }
-int64_t bwd_ctas(int d, int64_t T) { return ctas_of(d, T, bwd_rows(team_threads(d)), bwd_resident); }
+// Two steps are left to one CTA, which adds its sums to the gradients itself
+// (4 rows of 1,024: 27 us a call and 9.0 us a graph node; two CTAs and the
+// joining launch 30 and 8.3; with three steps the graph's node takes 10.5 and 8.9).
+constexpr int kOneCta = 2;
+int64_t bwd_ctas(int d, int64_t T) {
+  const int64_t ctas = ctas_of(d, T, bwd_rows(team_threads(d)), bwd_resident);
+  return ctas <= kOneCta ? 1 : ctas;
+}
 
 // 48 KB, the kernel's static arrays included, need no permission.
 template <typename K> cudaError_t allow_shared(K* kernel, int bytes) {
@@ -717,12 +726,14 @@ cudaError_t run_fwd(const hstu_config* c, const hstu_block_norm* n, const void* 
 }
 
 template <typename T, typename IO, int TPR>
-cudaError_t launch_bwd(const BwdArgs<T>& p, const void* y, const void* b, const void* dy, const void* dh,
+cudaError_t launch_bwd(BwdArgs<T> p, const void* y, const void* b, const void* dy, const void* dh,
                        void* dx, const GradPtrs& grads, cudaStream_t s) {
   constexpr int kBytes = bwd_rows(TPR) * kBwdSlots<T, IO, TPR>;
   cudaError_t e = allow_shared(block_norm_bwd_kernel<T, IO, TPR>, kBytes);
   if (e != cudaSuccess) return e;
   const int ctas = (int)bwd_ctas(p.d, p.rows);
+  p.grads = grads;
+  if (ctas == 1) p.partial = nullptr;
   block_norm_bwd_kernel<T, IO, TPR><<<(unsigned)ctas, kThreads<TPR>, kBytes, s>>>(
       p, static_cast<const IO*>(y), static_cast<const IO*>(b), static_cast<const IO*>(dy),
       static_cast<const IO*>(dh), static_cast<IO*>(dx));

@@ -35,6 +35,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 512;         // of a pass, at most
 constexpr int kMaxPasses = 4;
+constexpr int kJoinWords = 4;        // counters before the list of items to join, cleared by the sort
 constexpr int kAlone = 32;           // an item that goes on for more chunks is a long one
 // Up to this many tiles, a CTA of the sort adds up the tiles' counts by itself
 // (2 KB of each); above, a kernel of its own scans them once for all CTAs (two
@@ -182,13 +183,13 @@ struct Pass {
 };
 
 // Counts the first pass's digits of every tile, and clears the counts of the
-// later passes and of the items to join.
+// later passes and the counters before the list of items to join.
 __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(PairSource src, int64_t T, Pass pass, int passes,
                                                                  uint32_t* __restrict__ hist, int64_t pass_stride,
                                                                  uint32_t* __restrict__ joins) {
   __shared__ uint32_t h[kDigits];
   if (threadIdx.x < kDigits) h[threadIdx.x] = 0;
-  if (blockIdx.x == 0 && threadIdx.x < 2) joins[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < kJoinWords) joins[threadIdx.x] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * kTile;
 #pragma unroll
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(PairSource s
   __shared__ uint32_t warp_tot[kSortWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const uint32_t rank_of_cta = tc::cluster_rank();
-  if (blockIdx.x == 0 && tid < 2) joins[tid] = 0;
+  if (blockIdx.x == 0 && tid < kJoinWords) joins[tid] = 0;
   const int base = (int)blockIdx.x * kTile + warp * (32 * N) + lane;
   const int width = (bits + passes - 1) / passes;
   uint2 pair[N];
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(PairSource s
 }
 
 // All passes of T <= kSmallSort events, in shared memory; with heads, also
-// what heads_kernel and supers_kernel leave for the rows form.
+// what heads_kernel leaves for the rows form.
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src, int T, int bits, int passes,
                                                                   uint2* __restrict__ out,
                                                                   uint32_t* __restrict__ joins,
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src
   uint2* const buf = reinterpret_cast<uint2*>(dyn + kSortWarps * kDigits);              // [kSmallSort]
   __shared__ uint32_t warp_tot[kSortWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-  if (tid < 2) joins[tid] = 0;
+  if (tid < kJoinWords) joins[tid] = 0;
   // consecutive events in consecutive warps, as few rounds as T takes
   const int per = (T + kSortThreads - 1) / kSortThreads;
   const int base = warp * (32 * per) + lane;
@@ -539,12 +540,26 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(PairSource src
 // Rows form: how many items begin before each chunk
 // ---------------------------------------------------------------------------
 // heads[c]: items whose first event lies in an earlier chunk of chunk c's
-// kSuper events; supers[s]: in kSuper events number s.
+// kSuper events; supers[s]: in earlier kSuper events than number s; *num_rows:
+// in all.  A CTA counts kSuper events; the one that finishes last turns the counts
+// into prefix sums (*finished, cleared by the sort, tells).
 __global__ void __launch_bounds__(kSuper) heads_kernel(const uint2* __restrict__ pairs, int64_t T, uint32_t V,
                                                        int64_t chunks, uint32_t* __restrict__ heads,
-                                                       uint32_t* __restrict__ supers) {
-  __shared__ uint32_t warp_n[kSuper / 32];
+                                                       uint32_t* supers, uint32_t* finished,
+                                                       int64_t* __restrict__ num_rows) {
+  static_assert(kSuper == 32 * 32, "the warps' counts fit a warp");
+  __shared__ uint32_t warp_n[32];
+  __shared__ uint32_t carry;
+  __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto scan = [lane](uint32_t v) {        // inclusive, over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
   const int64_t t = (int64_t)blockIdx.x * kSuper + threadIdx.x;
   bool head = false;
   if (t < T) {
@@ -555,43 +570,31 @@ __global__ void __launch_bounds__(kSuper) heads_kernel(const uint2* __restrict__
   if (lane == 0) warp_n[warp] = n;
   __syncthreads();
   if (warp == 0) {
-    const uint32_t x = warp_n[lane];
-    uint32_t v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
+    const uint32_t x = warp_n[lane], v = scan(x);
     const int64_t c = (int64_t)blockIdx.x * (kSuper / kChunk) + lane;
     if (c < chunks) heads[c] = v - x;
-    if (lane == 31) supers[blockIdx.x] = v;
-  }
-}
-
-// supers becomes its exclusive prefix sum; *num_rows the number of items.  One CTA.
-__global__ void __launch_bounds__(1024) supers_kernel(uint32_t* __restrict__ supers, int64_t n,
-                                                      int64_t* __restrict__ num_rows) {
-  __shared__ uint32_t warp_tot[32];
-  __shared__ uint32_t carry;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) carry = 0;
-  __syncthreads();
-  for (int64_t base = 0; base < n; base += 1024) {
-    const int64_t i = base + threadIdx.x;
-    const uint32_t x = i < n ? supers[i] : 0u;
-    uint32_t v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += t;
+    if (lane == 31) {
+      supers[blockIdx.x] = v;
+      __threadfence();
+      last = atomicAdd(finished, 1u) == gridDim.x - 1;
+      carry = 0;
     }
-    if (lane == 31) warp_tot[warp] = v;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (uint32_t base = 0; base < gridDim.x; base += kSuper) {
+    const uint32_t i = base + threadIdx.x;
+    const uint32_t x = i < gridDim.x ? __ldcg(supers + i) : 0u, v = scan(x);
+    if (lane == 31) warp_n[warp] = v;
     __syncthreads();
-    uint32_t before = carry;
-    for (int w = 0; w < warp; ++w) before += warp_tot[w];
-    if (i < n) supers[i] = before + v - x;
+    uint32_t w = lane < warp ? warp_n[lane] : 0u;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    const uint32_t before = carry + w;
+    if (i < gridDim.x) supers[i] = before + v - x;
     __syncthreads();
-    if (threadIdx.x == 1023) carry = before + v;
+    if (threadIdx.x == kSuper - 1) carry = before + v;
     __syncthreads();
   }
   if (threadIdx.x == 0) *num_rows = carry;
@@ -615,7 +618,7 @@ struct SumArgs {
   // Items that cross chunks, by the chunk where they begin: joins[0] short ones
   // from the front of a list of [chunks], joins[1] long ones from its end.
   uint32_t* joins;
-  __device__ __forceinline__ uint32_t* list() const { return joins + 2; }
+  __device__ __forceinline__ uint32_t* list() const { return joins + kJoinWords; }
   // Items that begin before chunk c.
   __device__ __forceinline__ int64_t before(int64_t c) const {
     return (int64_t)supers[c / (kSuper / kChunk)] + heads[c];
@@ -859,7 +862,7 @@ BwdLayout bwd_layout(int64_t T, int dim) {
   l.heads = align_up(l.totals + kDigits * 4, 256);
   l.supers = align_up(l.heads + (size_t)l.chunks * 4, 256);
   l.joins = align_up(l.supers + (size_t)l.nsupers * 4, 256);
-  l.partial = align_up(l.joins + 8 + (size_t)l.chunks * 4, 256);
+  l.partial = align_up(l.joins + kJoinWords * 4 + (size_t)l.chunks * 4, 256);
   l.total = align_up(l.partial + (size_t)l.chunks * 2 * (size_t)dim * 4, 256);
   return l;
 }
@@ -999,9 +1002,9 @@ cudaError_t embedding_bwd(const void* dout, int dout_dtype, int64_t dout_stride,
   if (!row_ids)
     return dout_dtype == HSTU_BF16 ? launch_sum<bf16, false>(a, dout, s) : launch_sum<float, false>(a, dout, s);
   if (T > kSmallSort) {
-    heads_kernel<<<(unsigned)l.nsupers, kSuper, 0, s>>>(src.pairs, T, (uint32_t)V, l.chunks, heads, supers);
-    supers_kernel<<<1, 1024, 0, s>>>(supers, l.nsupers, num_rows);
-    count_launch(2);
+    heads_kernel<<<(unsigned)l.nsupers, kSuper, 0, s>>>(src.pairs, T, (uint32_t)V, l.chunks, heads, supers, joins + 2,
+                                                        num_rows);
+    count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
