@@ -625,32 +625,82 @@ struct SumArgs {
   }
 };
 
-template <int N> __device__ __forceinline__ void load_f(const float* p, float (&f)[N]) {
-  constexpr int M = N > 4 ? 4 : N;
-#pragma unroll
-  for (int i = 0; i < N; i += M) {
-    Pack<float, M> a;
-    a.load(p + i);
-#pragma unroll
-    for (int k = 0; k < M; ++k) f[i + k] = a.v[k];
+// The N columns of a lane in a slice of 32 N: neighbours, read and written in
+// one access (NEXT), or, where rows allow no wide access, 32 apart.
+template <int N, bool NEXT> struct Lane {
+  int col, have;        // the first column, and how many of the N there are
+  __device__ __forceinline__ explicit Lane(int dim) {
+    const int lane = threadIdx.x & 31;
+    col = (int)blockIdx.y * 32 * N + (NEXT ? lane * N : lane);
+    const int left = dim - col;
+    have = left <= 0 ? 0 : NEXT ? N : min(N, (left + 31) / 32);
+    if (!have) col = 0;
   }
-}
-template <int N> __device__ __forceinline__ void store_f(float* p, const float (&f)[N]) {
-  constexpr int M = N > 4 ? 4 : N;
+  // Of a row's elements from this lane's first column on.
+  template <typename T> __device__ __forceinline__ void load(const T* p, Pack<T, N>& a) const {
+    if constexpr (NEXT) {
+      a.load(p);
+    } else {
 #pragma unroll
-  for (int i = 0; i < N; i += M) {
-    Pack<float, M> a;
-#pragma unroll
-    for (int k = 0; k < M; ++k) a.v[k] = f[i + k];
-    a.store(p + i);
+      for (int k = 0; k < N; ++k) a.v[k] = k < have ? p[32 * k] : from_f<T>(0.f);
+    }
   }
-}
+  __device__ __forceinline__ void load(const float* p, float (&f)[N]) const {
+    if constexpr (NEXT) {
+      constexpr int M = N > 4 ? 4 : N;
+#pragma unroll
+      for (int i = 0; i < N; i += M) {
+        Pack<float, M> a;
+        a.load(p + i);
+#pragma unroll
+        for (int k = 0; k < M; ++k) f[i + k] = a.v[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) f[k] = k < have ? p[32 * k] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(float* p, const float (&f)[N]) const {
+    if constexpr (NEXT) {
+      constexpr int M = N > 4 ? 4 : N;
+#pragma unroll
+      for (int i = 0; i < N; i += M) {
+        Pack<float, M> a;
+#pragma unroll
+        for (int k = 0; k < M; ++k) a.v[k] = f[i + k];
+        a.store(p + i);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < have) p[32 * k] = f[k];
+    }
+  }
+  // load(), where the program says (volatile: the compiler would move each load of a
+  // batch down to its use, and wait for every one of them).
+  __device__ __forceinline__ void load_now(const float* p, float (&f)[N]) const {
+    if constexpr (NEXT && N >= 4) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(f[i]), "=f"(f[i + 1]), "=f"(f[i + 2]), "=f"(f[i + 3])
+                     : "l"(p + i)
+                     : "memory");
+    } else if constexpr (NEXT && N == 2) {
+      asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "l"(p) : "memory");
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(f[k]) : "l"(p + 32 * min(k, have - 1)) : "memory");
+    }
+  }
+};
 
-// A warp sums a chunk's columns [32 N y, 32 N (y + 1)); a lane owns N of them.
+// A warp sums a chunk's columns [32 N y, 32 N (y + 1)).
 // partial[c][0]: the sum of the item that came over from the chunk before;
 // partial[c][1]: of the one that begins in the chunk and goes on after it.
 // ROWS: items are written to their places in the rows form, else added.
-template <typename T, int N, bool ROWS>
+template <typename T, int N, bool NEXT, bool ROWS>
 __global__ void __launch_bounds__(256) sum_kernel(SumArgs a, const T* __restrict__ dout) {
   const int lane = threadIdx.x & 31;
   const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -669,10 +719,9 @@ __global__ void __launch_bounds__(256) sum_kernel(SumArgs a, const T* __restrict
   const uint32_t ends = __ballot_sync(0xffffffffu, real && right != mine.x);    // an item's last event
   const int count = __popc(__ballot_sync(0xffffffffu, real));   // padding sorts last
   if (count == 0) return;
-  const int col = ((int)blockIdx.y * 32 + lane) * N;
-  const bool live = col < a.dim;
-  const T* const src = dout + (live ? col : 0);
-  float* const dst = a.dst + (live ? col : 0);
+  const Lane<N, NEXT> cols(a.dim);
+  const T* const src = dout + cols.col;
+  float* const dst = a.dst + cols.col;
   const int64_t first_row = ROWS ? a.before(c) - 1 : 0;
   float acc[N];
 #pragma unroll
@@ -685,10 +734,11 @@ __global__ void __launch_bounds__(256) sum_kernel(SumArgs a, const T* __restrict
     for (int i = 0; i < kBatch; ++i) {
       const int j = j0 + i;
       const uint32_t key = __shfl_sync(0xffffffffu, mine.x, j & 31), ev = __shfl_sync(0xffffffffu, mine.y, j & 31);
-      if (j < count && live) {
-        row[i].load(src + (int64_t)ev * a.dout_stride);
+      if (j < count && cols.have) {
+        cols.load(src + (int64_t)ev * a.dout_stride, row[i]);
         // what the gradient holds of an item that begins and ends in this chunk
-        if (!ROWS && (ends >> j & 1u) && (begins & (0xffffffffu >> (31 - j)))) load_f<N>(dst + (int64_t)key * a.dst_stride, old[i]);
+        if (!ROWS && (ends >> j & 1u) && (begins & (0xffffffffu >> (31 - j))))
+          cols.load(dst + (int64_t)key * a.dst_stride, old[i]);
       }
     }
 #pragma unroll
@@ -702,18 +752,18 @@ __global__ void __launch_bounds__(256) sum_kernel(SumArgs a, const T* __restrict
       if (!end && j + 1 < count) continue;
       const uint32_t begun = begins & (0xffffffffu >> (31 - j));      // items begun so far
       if (!begun || !end) {
-        if (live) store_f<N>(a.partial + (c * 2 + (begun ? 1 : 0)) * a.dim + col, acc);
+        if (cols.have) cols.store(a.partial + (c * 2 + (begun ? 1 : 0)) * a.dim + cols.col, acc);
         if (begun && blockIdx.y == 0 && lane == 0) {
           const int is_long = far == key;
           const int64_t i = atomicAdd(a.joins + is_long, 1u);
           a.list()[is_long ? a.chunks - 1 - i : i] = (uint32_t)c;
         }
-      } else if (live) {
+      } else if (cols.have) {
         const int64_t at = ROWS ? first_row + __popc(begun) : (int64_t)key;
         float f[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) f[k] = ROWS ? a.scale * acc[k] : old[ROWS ? 0 : i][k] + a.scale * acc[k];
-        store_f<N>(dst + at * a.dst_stride, f);
+        cols.store(dst + at * a.dst_stride, f);
       }
       if (ROWS && begun && blockIdx.y == 0 && lane == 0) a.row_ids[first_row + __popc(begun)] = key;
 #pragma unroll
@@ -744,33 +794,17 @@ __device__ __forceinline__ int64_t last_chunk(const SumArgs& a, int64_t c, uint3
   }
 }
 
-// N floats, loaded where the program says (volatile: the compiler would move
-// each load of a batch down to its use, and wait for every one of them).
-template <int N> __device__ __forceinline__ void load_now(const float* p, float (&f)[N]) {
-  if constexpr (N >= 4) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(f[i]), "=f"(f[i + 1]), "=f"(f[i + 2]), "=f"(f[i + 3])
-                   : "l"(p + i)
-                   : "memory");
-  } else if constexpr (N == 2) {
-    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "l"(p) : "memory");
-  } else {
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(f[0]) : "l"(p) : "memory");
-  }
-}
-
 // Adds the partial sums of chunks first, first + STRIDE, ... up to last (at
 // least one), kFlight of them in flight; places past the last load that one again.
-template <int N, int STRIDE, int kFlight>
-__device__ __forceinline__ void add_partials(const SumArgs& a, int64_t first, int64_t last, int col, float (&acc)[N]) {
-  const float* p = a.partial + first * 2 * a.dim + col;
+template <int STRIDE, int kFlight, int N, bool NEXT>
+__device__ __forceinline__ void add_partials(const SumArgs& a, int64_t first, int64_t last, const Lane<N, NEXT>& cols,
+                                             float (&acc)[N]) {
+  const float* p = a.partial + first * 2 * a.dim + cols.col;
   const int64_t step = (int64_t)STRIDE * 2 * a.dim;
   for (int64_t left = (last - first) / STRIDE + 1; left > 0; left -= kFlight, p += kFlight * step) {
     float f[kFlight][N];
 #pragma unroll
-    for (int i = 0; i < kFlight; ++i) load_now<N>(p + min((int64_t)i, left - 1) * step, f[i]);
+    for (int i = 0; i < kFlight; ++i) cols.load_now(p + min((int64_t)i, left - 1) * step, f[i]);
 #pragma unroll
     for (int i = 0; i < kFlight; ++i)
 #pragma unroll
@@ -778,38 +812,38 @@ __device__ __forceinline__ void add_partials(const SumArgs& a, int64_t first, in
   }
 }
 
-template <int N, bool ROWS>
-__device__ __forceinline__ void put_joined(const SumArgs& a, int64_t c, uint32_t key, int col, const float (&acc)[N]) {
+template <bool ROWS, int N, bool NEXT>
+__device__ __forceinline__ void put_joined(const SumArgs& a, int64_t c, uint32_t key, const Lane<N, NEXT>& cols,
+                                           const float (&acc)[N]) {
   const int64_t at = ROWS ? a.before(c + 1) - 1 : (int64_t)key;
-  float* const p = a.dst + at * a.dst_stride + col;
+  float* const p = a.dst + at * a.dst_stride + cols.col;
   float f[N];
-  if (!ROWS) load_f<N>(p, f);
+  if (!ROWS) cols.load(p, f);
 #pragma unroll
   for (int k = 0; k < N; ++k) f[k] = ROWS ? a.scale * acc[k] : f[k] + a.scale * acc[k];
-  store_f<N>(p, f);
+  cols.store(p, f);
 }
 
 // Joins the partial sums of the listed items, columns [32 N y, 32 N (y + 1)) of
 // each: CTAs [0, longs) the long items, one at a time, whose warps add every
 // kJoinWarps-th chunk; the others the short ones, a warp each.
 constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
-template <int N, bool ROWS>
-__global__ void __launch_bounds__(kJoinThreads, N > 4 ? 2 : 3) join_kernel(SumArgs a, unsigned longs) {
+template <int N, bool NEXT, bool ROWS>
+__global__ void __launch_bounds__(kJoinThreads, N > 4 || !NEXT ? 2 : 3) join_kernel(SumArgs a, unsigned longs) {
   __shared__ float strip[kJoinWarps][32 * N];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int col = ((int)blockIdx.y * 32 + lane) * N;
-  const bool live = col < a.dim;
+  const Lane<N, NEXT> cols(a.dim);
   if (blockIdx.x >= longs) {
     const uint32_t items = a.joins[0];
     for (uint32_t i = (blockIdx.x - longs) * kJoinWarps + w; i < items; i += (gridDim.x - longs) * kJoinWarps) {
       const int64_t c = a.list()[i];
       const uint32_t key = a.pairs[(c + 1) * kChunk].x;
       const int64_t last = last_chunk(a, c, key);
-      if (!live) continue;
+      if (!cols.have) continue;
       float acc[N];
-      load_f<N>(a.partial + (c * 2 + 1) * a.dim + col, acc);
-      add_partials<N, 1, 4>(a, c + 1, last, col, acc);
-      put_joined<N, ROWS>(a, c, key, col, acc);
+      cols.load(a.partial + (c * 2 + 1) * a.dim + cols.col, acc);
+      add_partials<1, 4>(a, c + 1, last, cols, acc);
+      put_joined<ROWS>(a, c, key, cols, acc);
     }
     return;
   }
@@ -821,19 +855,19 @@ __global__ void __launch_bounds__(kJoinThreads, N > 4 ? 2 : 3) join_kernel(SumAr
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
-    if (live) {
-      if (w == 0) load_f<N>(a.partial + (c * 2 + 1) * a.dim + col, acc);
-      add_partials<N, kJoinWarps, 8>(a, c + 1 + w, last, col, acc);     // longer than kJoinWarps chunks
+    if (cols.have) {
+      if (w == 0) cols.load(a.partial + (c * 2 + 1) * a.dim + cols.col, acc);
+      add_partials<kJoinWarps, 8>(a, c + 1 + w, last, cols, acc);     // longer than kJoinWarps chunks
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) strip[w][k * 32 + lane] = acc[k];
     __syncthreads();
-    if (w == 0 && live) {
+    if (w == 0 && cols.have) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int o = 1; o < kJoinWarps; ++o) acc[k] += strip[o][k * 32 + lane];
-      put_joined<N, ROWS>(a, c, key, col, acc);
+      put_joined<ROWS>(a, c, key, cols, acc);
     }
     __syncthreads();
   }
@@ -878,10 +912,10 @@ hstu_status check_ids(const void* ids, int32_t id_bytes, int64_t T) {
 }
 hstu_status check_dtype(int32_t t) { return t == HSTU_F32 || t == HSTU_BF16 ? HSTU_OK : HSTU_ERR_INVALID; }
 
-template <typename T, int N, bool ROWS>
+template <typename T, int N, bool NEXT, bool ROWS>
 cudaError_t launch_sum_n(const SumArgs& a, const void* dout, cudaStream_t s) {
   const unsigned slices = (unsigned)((a.dim + 32 * N - 1) / (32 * N));
-  sum_kernel<T, N, ROWS><<<dim3((unsigned)((a.chunks + 7) / 8), slices), 256, 0, s>>>(a, static_cast<const T*>(dout));
+  sum_kernel<T, N, NEXT, ROWS><<<dim3((unsigned)((a.chunks + 7) / 8), slices), 256, 0, s>>>(a, static_cast<const T*>(dout));
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.chunks > 1) {
@@ -890,14 +924,15 @@ cudaError_t launch_sum_n(const SumArgs& a, const void* dout, cudaStream_t s) {
     const int64_t sms = sm_count(), most = (sms + slices - 1) / slices;
     const int64_t longs = std::min(most, (a.chunks + kAlone - 1) / kAlone);
     const int64_t shorts = std::min(2 * most, (a.chunks + kJoinWarps - 1) / kJoinWarps);
-    join_kernel<N, ROWS><<<dim3((unsigned)(longs + shorts), slices), kJoinThreads, 0, s>>>(a, (unsigned)longs);
+    join_kernel<N, NEXT, ROWS><<<dim3((unsigned)(longs + shorts), slices), kJoinThreads, 0, s>>>(a, (unsigned)longs);
     count_launch();
     e = cudaGetLastError();
   }
   return e;
 }
 // N columns a lane: 16 bytes of dout where alignment and width allow, fewer
-// rather than idle lanes for narrow rows.
+// rather than idle lanes for narrow rows; where rows allow no wide access, four
+// that are 32 apart (201,528 x 333: 184 us, 205 with one).
 template <typename T, bool ROWS>
 cudaError_t launch_sum(const SumArgs& a, const void* dout, cudaStream_t s) {
   constexpr int kMost = 16 / (int)sizeof(T);
@@ -906,10 +941,10 @@ cudaError_t launch_sum(const SumArgs& a, const void* dout, cudaStream_t s) {
                     vec_ok(n < 4 ? n : 4, a.dst, 4, a.dst_stride, a.dim, a.dim) && (n == 2 || a.dim > 16 * n)))
     n >>= 1;
   if constexpr (kMost == 8)
-    if (n == 8) return launch_sum_n<T, 8, ROWS>(a, dout, s);
-  return n == 4 ? launch_sum_n<T, 4, ROWS>(a, dout, s)
-         : n == 2 ? launch_sum_n<T, 2, ROWS>(a, dout, s)
-                  : launch_sum_n<T, 1, ROWS>(a, dout, s);
+    if (n == 8) return launch_sum_n<T, 8, true, ROWS>(a, dout, s);
+  if (n == 4) return launch_sum_n<T, 4, true, ROWS>(a, dout, s);
+  if (n == 2) return launch_sum_n<T, 2, true, ROWS>(a, dout, s);
+  return a.dim > 64 ? launch_sum_n<T, 4, false, ROWS>(a, dout, s) : launch_sum_n<T, 1, false, ROWS>(a, dout, s);
 }
 
 // The gradient in either form; rows form when row_ids is given.
