@@ -478,6 +478,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A buffer that kernels on this stream write (None: the current one): from the stream's own
+    pool, whose memory nothing that is still queued on another stream uses."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _launch(where, device, stream, f, *args, ws_bytes=None):
     """Calls the entry point f(*args[, workspace, bytes], stream) on the tensors' device.  A
     workspace comes from the caching allocator on the stream that the kernels run on, so that no
@@ -490,15 +499,12 @@ def _launch(where, device, stream, f, *args, ws_bytes=None):
             return _launch(where, device, stream, f, *args, ws_bytes=ws_bytes)
     if stream is None:
         s = _raw_stream(index)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
     else:
         if stream.device_index != index:
             raise ValueError(f"{where}: the stream belongs to cuda:{stream.device_index}, the tensors "
                              f"to {device}")
-        s, ws = stream.cuda_stream, None
-        if ws_bytes:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        s = stream.cuda_stream
+    ws = _empty(ws_bytes, torch.uint8, device, stream) if ws_bytes else None
     if ws_bytes is None:
         status = f(*args, s)
     else:
@@ -532,7 +538,7 @@ def embedding_fwd(table, ids, scale: float = 1.0, out=None, low=None, out_dtype=
     V, dim = table.shape
     ts = _rows(where, "table", table, V, dim, table.dtype, dev)
     if out is None:
-        out = torch.empty(T, dim, dtype=out_dtype, device=dev)
+        out = _empty((T, dim), out_dtype, dev, stream)
     if out.dtype not in _DTYPE_IDS or out.dim() != 2:
         raise ValueError(f"{where}: out must be [T][width] fp32 or bf16")
     width = out.shape[1]
@@ -650,11 +656,11 @@ def block_norm_fwd(cfg, bn: BlockNorm, x, b=None, gate=None, y=None, h=None, sta
     dev, d, T = x.device, cfg.d_model, x.shape[0]
     io, dt = torch_dtype(cfg.io_dtype), torch_dtype(cfg.dtype)
     if h is None and want_h:
-        h = torch.empty(T, d, dtype=dt, device=dev)
+        h = _empty((T, d), dt, dev, stream)
     if b is None:
         y, gate = x, None
     elif y is None:
-        y = torch.empty_like(x)
+        y = _empty((T, d), io, dev, stream)
     shape = (T, d)
     gs = 0 if gate is None else _rows(where, "gate", gate, T, d, dt, dev)
     _launch(where, dev, stream, lib().hstu_block_norm_fwd, ctypes.byref(cfg),
@@ -679,7 +685,7 @@ def block_norm_bwd(cfg, bn: BlockNorm, y, b, gate, stats, dy=None, dh=None, dx=N
     if dgate is not None and gate is None:
         raise ValueError(f"{where}: dgate needs gate")
     if dx is None:
-        dx = torch.empty(T, d, dtype=io, device=dev)
+        dx = _empty((T, d), io, dev, stream)
     shape = (T, d)
     gs = 0 if gate is None else _rows(where, "gate", gate, T, d, dt, dev)
     dgs = 0 if dgate is None else _rows(where, "dgate", dgate, T, d, dt, dev)

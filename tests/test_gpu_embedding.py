@@ -191,10 +191,32 @@ def test_offsets_past_32_bits():
     assert bool((g[V - 1] == 2).all()) and bool((g[0] == 1).all()) and float(g[1:V - 1].abs().max()) == 0
 
 
-def test_other_stream_and_graph():
-    """On a side stream, and captured: a replay reads the buffers' new contents; two graphs share no workspace."""
+def test_results_made_on_another_stream():
+    """A result that the call makes itself comes from the pool of the stream that writes it: memory that work still queued on
+    the current stream reads is not handed out for it."""
+    side = torch.cuda.Stream()
+    table, ids = torch.randn(50, 256, device=DEV), torch.arange(50, device=DEV).repeat(2000)
+    want = table[ids]
+    torch.cuda.synchronize()
+    sums = []
+    for _ in range(20):
+        old = torch.ones(100_000, 256, device=DEV)
+        for _ in range(4):
+            old = old * 1.0
+        sums.append(old.sum())
+        del old
+        out = H.embedding_fwd(table, ids, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(float(t) == 25_600_000 for t in sums)
+
+
+@pytest.mark.parametrize("T", [20, 700, 9000, 40_000])
+def test_other_stream_and_graph(T):
+    """On a side stream, and captured: a replay reads the buffers' new contents; two graphs share no workspace.  One size for
+    each form of the sort, and one chunk."""
     rng = np.random.default_rng(2)
-    T, V, dim = 700, 90, 40
+    V, dim = 90, 40
     side = torch.cuda.Stream()
     bufs = []
     for seed in (0, 1):
