@@ -13,18 +13,19 @@
 // Memory-bound (a token reads 10d bytes and writes 6d in the forward, reads
 // 16d and writes 8d in the backward, with bf16 operands and an fp32 residual
 // stream).  A team of TPR threads, 8 columns a thread (a power of two below a
-// warp, else whole warps), takes R rows at a time: 4 in the forward, 1 or 2 in the backward.  The columns stay the same, so the
-// parameters are read once and the gradients' sums stay in registers; the R
-// rows give the four sums that are joined together (4 means; 2 sums of 2
-// rows), at half the shuffles of four separate ones and one barrier.  The next
-// rows are on their way meanwhile: every thread copies its own elements of
-// them into its own slots of shared memory (cp.async), so the copies need no barrier.
-// The parameters' gradients are joined over the CTA's teams, written once per CTA and
-// summed over the CTAs by a second kernel, always in the same order.
+// warp, else whole warps), takes R rows at a time: 4 in the forward, 1 or 2 in
+// the backward.  The columns stay the same, so the parameters are read once and
+// the gradients' sums stay in registers; the R rows give the four sums that are
+// joined together (4 means; 2 sums of 2 rows), at half the shuffles of four
+// separate ones and one barrier.  The next rows are on their way meanwhile:
+// every thread copies its own elements of them into its own slots of shared
+// memory (cp.async), so the copies need no barrier.  The parameters' gradients
+// are joined over the CTA's teams, written once per CTA and summed over the
+// CTAs by a second kernel, always in the same order.
 //
 // Measured at 131,072 x 1,024, bf16 operands, fp32 residual stream: forward
-// 340 us (6.3 TB/s; 372 with 4 resident CTAs, which takes registers from
-// each), backward 546 us (6.4 TB/s; 599 with 3 CTAs; 566 with one row at a time and 4).
+// 340-343 us (6.3 TB/s; 372 with 4 resident CTAs, which takes registers from
+// each), backward 547 us (6.4 TB/s; 599 with 3 CTAs; 566 with one row at a time and 4).
 // With a bf16 residual stream (half the bytes, the same instructions) 0.7 of the copy rate.
 #include "args.h"
 #include "common.cuh"
