@@ -114,9 +114,11 @@ class ItemEmbedding:
         cap = min(ids.shape[0], V)
         if self.rows is None or self.rows.shape[0] != cap:
             dev = self.table.device
-            self.row_ids = torch.zeros(cap, dtype=torch.int64, device=dev)
-            self.rows = torch.zeros(cap, dim, dtype=torch.float32, device=dev)
-            self.count = torch.zeros(1, dtype=torch.int64, device=dev)
+            # cleared on the stream that writes them: a fill queued on another could come after
+            with torch.cuda.stream(stream):
+                self.row_ids = torch.zeros(cap, dtype=torch.int64, device=dev)
+                self.rows = torch.zeros(cap, dim, dtype=torch.float32, device=dev)
+                self.count = torch.zeros(1, dtype=torch.int64, device=dev)
         H.embedding_bwd_rows(dx, ids, V, self.row_ids, self.rows, self.count, self.scale, stream=stream)
 
     def zero_grad(self):

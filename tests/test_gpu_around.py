@@ -276,3 +276,21 @@ def test_wrong_stacks_are_refused():
         S.TrainStep(dw, ids=torch.zeros(dw.T, dtype=torch.int64, device=DEV))
     with pytest.raises(ValueError):
         S.NormedTrainStep(dw, [H.BlockNorm()] * 2)
+
+
+def test_rows_gradient_on_another_stream():
+    """The rows form's first call on a side stream while the current one is busy: the buffers that it makes are cleared on the
+    stream that writes them, so no fill comes after the gradient.  Sums of one 1.0 for each event are exact."""
+    side = torch.cuda.Stream()
+    ids = torch.arange(600, device=DEV).repeat(3)
+    dx = torch.ones(1800, 64, device=DEV)
+    emb = S.ItemEmbedding(torch.zeros(1000, 64, device=DEV), scale=1.0, rows=True)
+    busy = torch.ones(64 << 20, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(50):
+        busy.mul_(1.0)
+    emb.backward(dx, ids, stream=side)
+    torch.cuda.synchronize()
+    assert int(emb.count) == 600
+    assert torch.equal(emb.row_ids[:600], torch.arange(600, device=DEV))
+    assert torch.equal(emb.rows[:600], torch.full((600, 64), 3.0, device=DEV))
