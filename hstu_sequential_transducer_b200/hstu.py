@@ -655,10 +655,12 @@ def block_norm_fwd(cfg, bn: BlockNorm, x, b=None, gate=None, y=None, h=None, sta
     where = "block_norm_fwd"
     dev, d, T = x.device, cfg.d_model, x.shape[0]
     io, dt = torch_dtype(cfg.io_dtype), torch_dtype(cfg.dtype)
+    if b is None and (gate is not None or (y is not None and y is not x)):
+        raise ValueError(f"{where}: gate and y need b (without it y is x)")
     if h is None and want_h:
         h = _empty((T, d), dt, dev, stream)
     if b is None:
-        y, gate = x, None
+        y = x
     elif y is None:
         y = _empty((T, d), io, dev, stream)
     shape = (T, d)

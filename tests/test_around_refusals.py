@@ -139,3 +139,11 @@ def test_binding_refuses_wrong_tensors(L):
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+def test_joint_without_block_output():
+    """Without b there is nothing to gate and no new y: a call that passes either is refused, not answered without it."""
+    x = torch.zeros(4, 64)
+    for kw in ({"gate": torch.zeros(4, 64, dtype=torch.bfloat16)}, {"y": torch.zeros(4, 64)}):
+        with pytest.raises(ValueError, match="need b"):
+            H.block_norm_fwd(cfg(), H.BlockNorm(), x, **kw)
