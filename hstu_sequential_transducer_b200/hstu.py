@@ -268,17 +268,19 @@ def saved_views(cfg: Config, saved: torch.Tensor, T: int):
     return out
 
 
-_ws_cache = {}
+def _empty(shape, dtype, device, stream):
+    """A buffer that kernels on this stream write (None: the current one): from the stream's own
+    pool, whose memory nothing that is still queued on another stream uses."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def workspace(nbytes: int, device, key="default") -> torch.Tensor:
-    """A cached uint8 device buffer of at least nbytes (allocated by torch)."""
-    k = (str(device), key)
-    t = _ws_cache.get(k)
-    if t is None or t.numel() < nbytes:
-        t = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _ws_cache[k] = t
-    return t
+def workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    """Scratch of one call, at least nbytes: a new buffer each time, on the stream that the call's
+    kernels run on, so that no two calls, streams or captured graphs share one."""
+    return _empty((max(nbytes, 256),), torch.uint8, device, stream)
 
 
 # ----------------------------------------------------------------------------
@@ -296,7 +298,7 @@ def attention_fwd(cfg, rab_pos, rab_time, g, offsets, timestamps, num_targets, o
     hstu_attention_workspace_size)."""
     B, T = offsets.numel() - 1, g.shape[0]
     n = lib().hstu_attention_workspace_size(ctypes.byref(cfg), B, T)
-    ws = workspace(n, g.device, "attn")
+    ws = workspace(n, g.device, stream)
     nb = ws.numel() if ws_bytes is None else min(int(ws_bytes), ws.numel())
     _check(lib().hstu_attention_fwd(ctypes.byref(cfg), ptr(rab_pos), ptr(rab_time), ptr(g),
                                     ptr(offsets), B, T, ptr(timestamps), ptr(num_targets),
@@ -309,7 +311,7 @@ def softmax_attention_fwd(cfg, rab_pos, rab_time, g, offsets, timestamps, num_ta
     """The softmax comparison attention (same score and mask, softmax weights)."""
     B, T = offsets.numel() - 1, g.shape[0]
     n = lib().hstu_attention_workspace_size(ctypes.byref(cfg), B, T)
-    ws = workspace(n, g.device, "attn")
+    ws = workspace(n, g.device, stream)
     _check(lib().hstu_softmax_attention_fwd(ctypes.byref(cfg), ptr(rab_pos), ptr(rab_time), ptr(g),
                                             ptr(offsets), B, T, ptr(timestamps), ptr(num_targets),
                                             ptr(o_out), ptr(ws), ws.numel(), stream_ptr(stream)),
@@ -330,7 +332,7 @@ def attention_fwd_cached(cfg, rab_pos, rab_time, cand_g, cand_offsets, cand_ts, 
                          hist_offsets, hist_ts, o_out, stream=None):
     B, Tc, Th = cand_offsets.numel() - 1, cand_g.shape[0], hist_kv.shape[0]
     n = lib().hstu_attention_workspace_size(ctypes.byref(cfg), B, Tc)
-    ws = workspace(n, cand_g.device, "attn")
+    ws = workspace(n, cand_g.device, stream)
     _check(lib().hstu_attention_fwd_cached(ctypes.byref(cfg), ptr(rab_pos), ptr(rab_time),
                                            ptr(cand_g), ptr(cand_offsets), B, Tc, ptr(cand_ts),
                                            ptr(hist_kv), ptr(hist_offsets), Th, ptr(hist_ts),
@@ -367,7 +369,7 @@ def attention_bwd(cfg, rab_pos, rab_time, g, pre, dout, offsets, timestamps, num
                   drab_pos=None, drab_time=None, stream=None):
     B, T = offsets.numel() - 1, g.shape[0]
     n = lib().hstu_attention_bwd_workspace_size(ctypes.byref(cfg), B, T)
-    ws = workspace(n, g.device, "attn_bwd")
+    ws = workspace(n, g.device, stream)
     _check(lib().hstu_attention_bwd(ctypes.byref(cfg), ptr(rab_pos), ptr(rab_time), ptr(g), ptr(pre),
                                     ptr(dout), ptr(offsets), B, T, ptr(timestamps),
                                     ptr(num_targets), ptr(dpre), ptr(drab_pos), ptr(drab_time),
@@ -478,19 +480,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _empty(shape, dtype, device, stream):
-    """A buffer that kernels on this stream write (None: the current one): from the stream's own
-    pool, whose memory nothing that is still queued on another stream uses."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
 def _launch(where, device, stream, f, *args, ws_bytes=None):
-    """Calls the entry point f(*args[, workspace, bytes], stream) on the tensors' device.  A
-    workspace comes from the caching allocator on the stream that the kernels run on, so that no
-    two calls, streams or captured graphs share one."""
+    """Calls the entry point f(*args[, workspace, bytes], stream) on the tensors' device, with
+    a workspace of this call alone."""
     if device.type != "cuda":
         raise ValueError(f"{where}: needs CUDA tensors, got {device}")
     index = device.index
@@ -768,7 +760,7 @@ def fwd(cfg, w: LayerWeights, x, offsets, timestamps, num_targets=None, y=None, 
     the bf16 copy of y for the next one (hstu_fwd_chain)."""
     B, T = offsets.numel() - 1, x.shape[0]
     ws_n, _ = workspace_size(cfg, B, T)
-    ws = workspace(ws_n, x.device)
+    ws = workspace(ws_n, x.device, stream)
     if y is None:
         y = torch.empty_like(x)
     if x_low is None and y_low is None:
@@ -787,7 +779,7 @@ def fwd_cached(cfg, w: LayerWeights, cand_x, cand_offsets, cand_ts, hist_kv, his
                y=None, stream=None):
     B, Tc = cand_offsets.numel() - 1, cand_x.shape[0]
     ws_n, _ = workspace_size(cfg, B, Tc)
-    ws = workspace(ws_n, cand_x.device)
+    ws = workspace(ws_n, cand_x.device, stream)
     if y is None:
         y = torch.empty_like(cand_x)
     _check(lib().hstu_fwd_cached(ctypes.byref(cfg), ctypes.byref(w.c()), ptr(cand_x),
@@ -804,7 +796,7 @@ def bwd(cfg, w: LayerWeights, x, dy, saved, offsets, timestamps, num_targets=Non
     bf16 copy of dx for the layer below (hstu_bwd_chain)."""
     B, T = offsets.numel() - 1, x.shape[0]
     ws_n, _ = workspace_size(cfg, B, T)
-    ws = workspace(ws_n, x.device)
+    ws = workspace(ws_n, x.device, stream)
     if dx is None:
         dx = torch.empty_like(x)
     g = grads.c() if grads is not None else Grads()

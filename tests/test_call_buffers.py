@@ -1,0 +1,78 @@
+"""Which buffers the Python calls make, and where (CPU only): the library's launches are replaced by a recorder, its host-side
+size queries are its own."""
+import ctypes
+import types
+
+import pytest
+import torch
+
+from hstu_sequential_transducer_b200 import build
+from hstu_sequential_transducer_b200 import hstu as H
+
+
+class Recorder:
+    """The library with its launches recorded: (name, arguments) of each."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name.endswith(("_size", "_layout", "_string")):
+            return getattr(self.real, name)
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    build.build()
+    rec = Recorder(H.lib())
+    monkeypatch.setattr(H, "lib", lambda: rec)
+    monkeypatch.setattr(H, "stream_ptr", lambda s=None: None if s is None else s.cuda_stream)
+    return rec
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """Every buffer that a call makes: (tensor, stream)."""
+    out = []
+    real = torch.empty
+
+    def empty(shape, dtype, device, stream):
+        out.append((real(shape, dtype=dtype, device=device), stream))
+        return out[-1][0]
+    monkeypatch.setattr(H, "_empty", empty)
+    return out
+
+
+def layer(T=40, d=64):
+    cfg = H.make_config(d, 2, 64.0)
+    z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t)
+    low = lambda *s: z(*s, t=torch.bfloat16)
+    w = H.LayerWeights(W1=low(d, 4 * d), W2=low(d, d))
+    off, ts = torch.tensor([0, T // 2, T]), z(T, t=torch.int64)
+    saved = z(H.saved_layout(cfg, T)[-1], t=torch.uint8)
+    return {"fwd": lambda s: H.fwd(cfg, w, z(T, d), off, ts, y=z(T, d), stream=s),
+            "bwd": lambda s: H.bwd(cfg, w, z(T, d), z(T, d), saved, off, ts, dx=z(T, d), stream=s),
+            "fwd_cached": lambda s: H.fwd_cached(cfg, w, z(T, d), off, ts, low(T, 2 * d), off, ts, y=z(T, d), stream=s),
+            "attention_fwd": lambda s: H.attention_fwd(cfg, None, None, low(T, 4 * d), off, ts, None, z(T, d), stream=s),
+            "softmax_attention_fwd": lambda s: H.softmax_attention_fwd(cfg, None, None, low(T, 4 * d), off, ts, None, z(T, d), stream=s),
+            "attention_fwd_cached": lambda s: H.attention_fwd_cached(cfg, None, None, low(T, 4 * d), off, ts, low(T, 2 * d), off, ts,
+                                                                     z(T, d), stream=s),
+            "attention_bwd": lambda s: H.attention_bwd(cfg, None, None, low(T, 4 * d), low(T, 4 * d), z(T, d), off, ts, None,
+                                                       low(T, 4 * d), stream=s)}
+
+
+@pytest.mark.parametrize("call", sorted(layer()))
+def test_scratch_belongs_to_one_call_on_its_stream(lib, made, call):
+    """Two calls on two streams run side by side, so each has scratch of its own, from its own stream's pool; nothing that an
+    earlier call (or a graph captured from it) uses is kept for a later one or let go by it."""
+    a, b = types.SimpleNamespace(cuda_stream=11), types.SimpleNamespace(cuda_stream=22)
+    f = layer()[call]
+    for stream in (a, b, None):
+        f(stream)
+    assert [s for _, s in made] == [a, b, None]
+    used = [[x for x in args if isinstance(x, int)] for _, args in lib.calls]
+    for (t, s), ints in zip(made, used):
+        assert t.data_ptr() in ints and t.numel() in ints
+        assert s is None or s.cuda_stream in ints
+    assert len({t.data_ptr() for t, _ in made}) == 3

@@ -1,0 +1,89 @@
+"""Training steps on several streams at once, and captured beside eager ones: each call's scratch is its own.
+
+Two runs of a step on the same inputs differ only by the order in which the backward's atomic sums arrive, a few roundings
+u of the sums' terms (2^-24 each for fp32 sums, 2^-8 where a bf16 operand in between flips): normwise within 1e-4 (f32) and
+1e-2 (bf16) of one another.  Forward outputs are equal bit for bit."""
+import pytest
+import torch
+
+from hstu_sequential_transducer_b200 import build
+from hstu_sequential_transducer_b200 import hstu as H
+from hstu_sequential_transducer_b200 import stack as S
+from hstu_sequential_transducer_b200 import workloads as W
+
+pytestmark = pytest.mark.gpu
+TOL = {"f32": 1e-4, "bf16": 1e-2}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    H.lib()
+
+
+def batch(dtype, lengths, seed, layers=3):
+    return S.DeviceWorkload.from_workload(W.custom(lengths, d=128, H=2, dtype=dtype, N=400.0, with_bias=True, with_affine=True,
+                                                   backward=True, layers=layers, mean_gap=900.0, seed=seed))
+
+
+def make(kind, dw):
+    if kind == "train":
+        return S.TrainStep(dw)
+    return S.NormedTrainStep(dw, [H.BlockNorm() for _ in range(len(dw.layers) + 1)])
+
+
+def parts(kind, step, dx):
+    grads = [t for g in step.grads for t in vars(g).values() if t is not None]
+    return [step.y.clone()] + [t.clone() for t in (dx, *grads)]
+
+
+def same(got, want, dtype):
+    assert torch.equal(got[0], want[0])
+    for a, b in zip(got[1:], want[1:]):
+        a, b = a.double(), b.double()
+        assert float((a - b).norm()) <= TOL[dtype] * float(b.norm())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["train", "normed"])
+def test_two_streams(kind, dtype):
+    dws = [batch(dtype, [300, 17, 0, 250, 399], 1), batch(dtype, [128, 399, 64, 1], 2)]
+    steps = [make(kind, dw) for dw in dws]
+    want = []
+    for s in steps:
+        s.zero_grads()
+        want.append(parts(kind, s, s.run()))
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(4):
+        for s in steps:
+            s.zero_grads()
+        torch.cuda.synchronize()
+        dx = [s.run(stream=st) for s, st in zip(steps, streams)]
+        torch.cuda.synchronize()
+        for s, d, w in zip(steps, dx, want):
+            same(parts(kind, s, d), w, dtype)
+
+
+@pytest.mark.parametrize("kind", ["train", "normed"])
+def test_captured_step_after_a_larger_eager_one(kind):
+    """A graph keeps its own scratch: a later eager step that needs more lets none of it go."""
+    small, large = make(kind, batch("bf16", [60, 33], 3)), make(kind, batch("bf16", [399] * 12, 4))
+
+    def one(step):
+        step.zero_grads()
+        return step.run()
+
+    want = parts(kind, small, one(small))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx = one(small)
+    big = parts(kind, large, one(large))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    fresh = torch.full((64 << 20,), 7.0, device="cuda")              # what the allocator hands out next
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    same(parts(kind, small, dx), want, "bf16")
+    assert bool((fresh == 7.0).all())
+    same(parts(kind, large, one(large)), big, "bf16")
