@@ -277,6 +277,11 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t, stream):
+    """A contiguous buffer of t's shape and type for kernels on this stream."""
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
 def workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     """Scratch of one call, at least nbytes: a new buffer each time, on the stream that the call's
     kernels run on, so that no two calls, streams or captured graphs share one."""
@@ -386,11 +391,12 @@ def validate_inputs(offsets, timestamps, num_targets, max_seq_len, stream=None) 
     """Runs the device validator and returns its flag word (synchronises)."""
     B = offsets.numel() - 1
     T = timestamps.numel()
-    flags = torch.zeros(1, dtype=torch.int32, device=offsets.device)
-    _check(lib().hstu_validate_inputs(ptr(offsets), B, T, ptr(timestamps), ptr(num_targets),
-                                      max_seq_len, ptr(flags), stream_ptr(stream)),
-           "hstu_validate_inputs")
-    return int(flags.item())
+    with torch.cuda.stream(stream):            # the flags are cleared and read on the validator's stream
+        flags = torch.zeros(1, dtype=torch.int32, device=offsets.device)
+        _check(lib().hstu_validate_inputs(ptr(offsets), B, T, ptr(timestamps), ptr(num_targets),
+                                          max_seq_len, ptr(flags), stream_ptr(stream)),
+               "hstu_validate_inputs")
+        return int(flags.item())
 
 
 # ----------------------------------------------------------------------------
@@ -419,9 +425,9 @@ def stochastic_length(offsets, num_targets, sub_len, keep_draw, keys, new_offset
     if keep_draw.numel() != B:
         raise ValueError("stochastic_length: keep_draw needs one entry per sequence")
     if new_offsets is None:
-        new_offsets = torch.empty(B + 1, dtype=torch.int64, device=offsets.device)
+        new_offsets = _empty((B + 1,), torch.int64, offsets.device, stream)
     if gather_index is None:
-        gather_index = torch.empty(max(T, 1), dtype=torch.int64, device=offsets.device)
+        gather_index = _empty((max(T, 1),), torch.int64, offsets.device, stream)
     _check(lib().hstu_stochastic_length(ptr(offsets), ptr(num_targets), B, T, int(sub_len),
                                         ptr(keep_draw), ptr(keys), ptr(new_offsets),
                                         ptr(gather_index), stream_ptr(stream)),
@@ -762,7 +768,7 @@ def fwd(cfg, w: LayerWeights, x, offsets, timestamps, num_targets=None, y=None, 
     ws_n, _ = workspace_size(cfg, B, T)
     ws = workspace(ws_n, x.device, stream)
     if y is None:
-        y = torch.empty_like(x)
+        y = _like(x, stream)
     if x_low is None and y_low is None:
         _check(lib().hstu_fwd(ctypes.byref(cfg), ctypes.byref(w.c()), ptr(x), ptr(offsets), B, T,
                               ptr(timestamps), ptr(num_targets), ptr(y), ptr(saved), ptr(kv_out),
@@ -781,7 +787,7 @@ def fwd_cached(cfg, w: LayerWeights, cand_x, cand_offsets, cand_ts, hist_kv, his
     ws_n, _ = workspace_size(cfg, B, Tc)
     ws = workspace(ws_n, cand_x.device, stream)
     if y is None:
-        y = torch.empty_like(cand_x)
+        y = _like(cand_x, stream)
     _check(lib().hstu_fwd_cached(ctypes.byref(cfg), ctypes.byref(w.c()), ptr(cand_x),
                                  ptr(cand_offsets), B, Tc, ptr(cand_ts), ptr(hist_kv),
                                  ptr(hist_offsets), hist_kv.shape[0], ptr(hist_ts), ptr(y), ptr(ws),
@@ -798,7 +804,7 @@ def bwd(cfg, w: LayerWeights, x, dy, saved, offsets, timestamps, num_targets=Non
     ws_n, _ = workspace_size(cfg, B, T)
     ws = workspace(ws_n, x.device, stream)
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = _like(x, stream)
     g = grads.c() if grads is not None else Grads()
     if dy_low is None and dx_low is None:
         _check(lib().hstu_bwd(ctypes.byref(cfg), ctypes.byref(w.c()), ptr(x), ptr(dy), ptr(saved),

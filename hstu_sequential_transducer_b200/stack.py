@@ -81,7 +81,7 @@ def forward_stack(dw: DeviceWorkload, num_layers: Optional[int] = None, stream=N
     lo = []
     if ch:
         lt = H.torch_dtype(dw.cfg.dtype)
-        lo = [torch.empty(dw.T, dw.cfg.d_model, dtype=lt, device=dw.x.device) for _ in range(2)]
+        lo = [H._empty((dw.T, dw.cfg.d_model), lt, dw.x.device, stream) for _ in range(2)]
     for i, w in enumerate(layers):
         y = H.fwd(dw.cfg, w, y, dw.offsets, dw.timestamps, dw.num_targets, stream=stream,
                   x_low=lo[i % 2] if ch and i > 0 else None,
@@ -364,7 +364,13 @@ def mfalcon_score(dw: DeviceWorkload, history: int, candidates: int, microbatch:
     by `candidates` tokens: one history pass caching each layer's V|K, then the
     candidates in microbatches against the cache.  Returns (y_hist, y_cand)
     with candidate rows in input order.  Row selection and reordering run in
-    the library's gather kernel."""
+    the library's gather kernel.
+    Everything, the row selection included, runs on the stream (None: the current one)."""
+    with torch.cuda.stream(stream):
+        return _mfalcon_score(dw, history, candidates, microbatch)
+
+
+def _mfalcon_score(dw: DeviceWorkload, history: int, candidates: int, microbatch: int):
     w = dw.w
     B = w.B
     dev = dw.x.device
@@ -380,7 +386,7 @@ def mfalcon_score(dw: DeviceWorkload, history: int, candidates: int, microbatch:
     y = x_hist
     for lw in dw.layers:
         kv = torch.empty(y.shape[0], 2 * d, dtype=H.torch_dtype(dw.cfg.dtype), device=dev)
-        y = H.fwd(dw.cfg, lw, y, hist_off, ts_hist, None, kv_out=kv, stream=stream)
+        y = H.fwd(dw.cfg, lw, y, hist_off, ts_hist, None, kv_out=kv)
         caches.append(kv)
     y_hist = y
     # microbatch k writes its B * mb_k rows (user-major) into its own slice of
@@ -398,7 +404,7 @@ def mfalcon_score(dw: DeviceWorkload, history: int, candidates: int, microbatch:
         for li, lw in enumerate(dw.layers):
             last = li == len(dw.layers) - 1
             xc = H.fwd_cached(dw.cfg, lw, xc, coff, tc, caches[li], hist_off, ts_hist,
-                              y=out if last else None, stream=stream)
+                              y=out if last else None)
         src_rows[:, k0:k0 + mb] = done + np.arange(B)[:, None] * mb + np.arange(mb)[None, :]
         done += B * mb
     y_cand = _gather(ybuf, src_rows.reshape(-1))

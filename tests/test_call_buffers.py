@@ -76,3 +76,22 @@ def test_scratch_belongs_to_one_call_on_its_stream(lib, made, call):
         assert t.data_ptr() in ints and t.numel() in ints
         assert s is None or s.cuda_stream in ints
     assert len({t.data_ptr() for t, _ in made}) == 3
+
+
+def test_results_come_from_the_stream_that_writes_them(lib, made):
+    """What a call makes for its caller when given no buffer: on the call's stream, like its scratch."""
+    T, d = 40, 64
+    cfg = H.make_config(d, 2, 64.0)
+    z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t)
+    w = H.LayerWeights(W1=z(d, 4 * d, t=torch.bfloat16), W2=z(d, d, t=torch.bfloat16))
+    off, ts = torch.tensor([0, 20, T]), z(T, t=torch.int64)
+    side = types.SimpleNamespace(cuda_stream=11)
+    saved = z(H.saved_layout(cfg, T)[-1], t=torch.uint8)
+    out = [H.fwd(cfg, w, z(T, d), off, ts, stream=side),
+           H.fwd_cached(cfg, w, z(T, d), off, ts, z(T, 2 * d, t=torch.bfloat16), off, ts, stream=side),
+           H.bwd(cfg, w, z(T, d), z(T, d), saved, off, ts, stream=side),
+           *H.stochastic_length(off, None, 5, z(2), z(T), stream=side)]
+    assert all(s is side for _, s in made)
+    for t in out:
+        assert any(t is m for m, _ in made)
+    assert [tuple(t.shape) for t in out] == [(T, d)] * 3 + [(3,), (T,)]

@@ -87,3 +87,21 @@ def test_captured_step_after_a_larger_eager_one(kind):
     same(parts(kind, small, dx), want, "bf16")
     assert bool((fresh == 7.0).all())
     same(parts(kind, large, one(large)), big, "bf16")
+
+
+def test_forward_and_scoring_on_a_side_stream():
+    """The whole of a forward stack and of cached scoring runs on the given stream while the current one is busy: rows are
+    selected, and buffers in between come and go, on it."""
+    w = W.custom([170] * 3, d=128, H=2, dtype="bf16", N=400.0, layers=3, mean_gap=900.0, seed=5, num_targets=[70] * 3)
+    dw = S.DeviceWorkload.from_workload(w)
+    want = [S.forward_stack(dw), *S.mfalcon_score(dw, 100, 70, 32)]
+    side, busy = torch.cuda.Stream(), torch.ones(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(20):
+            busy.mul_(1.0)
+        got = [S.forward_stack(dw, stream=side), *S.mfalcon_score(dw, 100, 70, 32, stream=side)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert H.validate_inputs(dw.offsets, dw.timestamps, dw.num_targets, 400, stream=side) == 0
