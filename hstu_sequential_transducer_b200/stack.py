@@ -24,6 +24,20 @@ def _t(a, dtype, device):
     return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to(device=device, dtype=dtype)
 
 
+def _settled(device):
+    """Ends a constructor: waits until what it queued has run, so that a first use on any stream
+    comes after it (a fill of a gradient still queued on another stream would erase it)."""
+    if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+
+
+def _zero(tensors, stream):
+    with torch.cuda.stream(stream):
+        for t in tensors:
+            if t is not None:
+                t.zero_()
+
+
 @dataclass
 class DeviceWorkload:
     cfg: H.Config
@@ -99,6 +113,7 @@ class ItemEmbedding:
         self.scale = float(table.shape[1]) ** 0.5 if scale is None else float(scale)
         self.grad = None if rows else torch.zeros(table.shape, dtype=torch.float32, device=table.device)
         self.row_ids = self.rows = self.count = None
+        _settled(table.device)
 
     def lookup(self, ids, out, low=None, stream=None):
         """out[t] = scale * table[ids[t]], zero for padding ids and for columns past dim."""
@@ -121,9 +136,9 @@ class ItemEmbedding:
                 self.count = torch.zeros(1, dtype=torch.int64, device=dev)
         H.embedding_bwd_rows(dx, ids, V, self.row_ids, self.rows, self.count, self.scale, stream=stream)
 
-    def zero_grad(self):
-        if self.grad is not None:
-            self.grad.zero_()
+    def zero_grad(self, stream=None):
+        """Clears the dense gradient, on the stream that the next backward runs on."""
+        _zero([self.grad], stream)
 
 
 CHECKPOINTS = {"int8": H.CKPT_INT8, "e4m3": H.CKPT_E4M3}
@@ -223,9 +238,11 @@ class TrainStep:
                     o += (t.numel() + 63) // 64 * 64
             self.grads.append(gb)
             self.layer_grad_sizes.append(o - o0)
+        _settled(dev)
 
-    def zero_grads(self):
-        self.flat_grads.zero_()
+    def zero_grads(self, stream=None):
+        """Clears the layers' gradients, on the stream that the next run is given."""
+        _zero([self.flat_grads], stream)
 
     def run(self, dy=None, stream=None, on_layer_grads=None):
         """Forward (keeping activations) then backward from dy; returns dX.
@@ -299,12 +316,11 @@ class NormedTrainStep:
         self.db, self.dz, self.do = low(), low(), low()
         self.dpre = torch.empty(T, 4 * d, dtype=dt, device=dev)
         self.dh, self.dy = torch.empty_like(dw.x), torch.empty_like(dw.x)
+        _settled(dev)
 
-    def zero_grads(self):
-        for g in (*self.grads, *self.joint_grads):
-            for t in vars(g).values():
-                if t is not None:
-                    t.zero_()
+    def zero_grads(self, stream=None):
+        """Clears the gradients of the layers and joints, on the stream that the next run is given."""
+        _zero([t for g in (*self.grads, *self.joint_grads) for t in vars(g).values()], stream)
 
     @property
     def y(self):

@@ -8,6 +8,8 @@ import torch
 
 from hstu_sequential_transducer_b200 import build
 from hstu_sequential_transducer_b200 import hstu as H
+from hstu_sequential_transducer_b200 import stack as S
+from hstu_sequential_transducer_b200 import workloads as W
 
 
 class Recorder:
@@ -95,3 +97,34 @@ def test_results_come_from_the_stream_that_writes_them(lib, made):
     for t in out:
         assert any(t is m for m, _ in made)
     assert [tuple(t.shape) for t in out] == [(T, d)] * 3 + [(3,), (T,)]
+
+
+def test_gradients_are_cleared_on_the_given_stream(monkeypatch):
+    """zero_grad(s) before a run on a side stream: the fill is queued there, in front of the run."""
+    build.build()
+    w = W.custom([9, 4], d=64, H=2, dtype="bf16", N=16.0, backward=True, layers=2)
+    dw = S.DeviceWorkload.from_workload(w, device="cpu")
+    emb, train = S.ItemEmbedding(torch.zeros(5, 64)), S.TrainStep(dw)
+    normed = S.NormedTrainStep(dw, [H.BlockNorm() for _ in range(3)])
+    current, fills = [None], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    real = torch.Tensor.zero_
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: (fills.append(current[-1]), real(t))[1])
+    for clear, filled in ((emb.zero_grad, [emb.grad]), (train.zero_grads, [train.flat_grads]),
+                          (normed.zero_grads, [t for g in normed.grads for t in vars(g).values() if t is not None])):
+        for t in filled:
+            t.fill_(3.0)
+        fills.clear()
+        clear(stream="side")
+        assert set(fills) == {"side"} and all(not bool(t.any()) for t in filled)
+        clear()

@@ -105,3 +105,44 @@ def test_forward_and_scoring_on_a_side_stream():
         for a, b in zip(got, want):
             assert torch.equal(a, b)
     assert H.validate_inputs(dw.offsets, dw.timestamps, dw.num_targets, 400, stream=side) == 0
+
+
+def test_gradient_on_a_side_stream_behind_a_busy_current_one():
+    """The dense gradient's first use and its clearing, on a side stream while the current one has work queued: no fill comes
+    after a gradient.  Sums of one 1.0 for each event are exact."""
+    side, busy = torch.cuda.Stream(), torch.ones(64 << 20, device="cuda")
+    ids, dx, table = torch.arange(600, device="cuda").repeat(3), torch.ones(1800, 64, device="cuda"), torch.zeros(1000, 64, device="cuda")
+    want = torch.zeros(1000, 64, device="cuda")
+    want[:600] = 3.0
+    torch.cuda.synchronize()
+    for _ in range(50):
+        busy.mul_(1.0)
+    emb = S.ItemEmbedding(table, scale=1.0)
+    emb.backward(dx, ids, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(emb.grad, want)
+    for _ in range(50):
+        busy.mul_(1.0)
+    emb.zero_grad(stream=side)
+    emb.backward(dx, ids, stream=side)
+    side.synchronize()
+    assert torch.equal(emb.grad, want)
+
+
+@pytest.mark.parametrize("kind", ["train", "normed"])
+def test_first_run_on_a_side_stream_behind_a_busy_current_one(kind):
+    dw = batch("bf16", [60, 33], 3)
+    serial = make(kind, dw)
+    want = parts(kind, serial, serial.run())
+    side, busy = torch.cuda.Stream(), torch.ones(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    for again in (False, True):
+        for _ in range(50):
+            busy.mul_(1.0)
+        if again:
+            step.zero_grads(stream=side)
+        else:
+            step = make(kind, dw)
+        dx = step.run(stream=side)
+        torch.cuda.synchronize()
+        same(parts(kind, step, dx), want, "bf16")
