@@ -113,6 +113,8 @@ class ItemEmbedding:
         self.scale = float(table.shape[1]) ** 0.5 if scale is None else float(scale)
         self.grad = None if rows else torch.zeros(table.shape, dtype=torch.float32, device=table.device)
         self.row_ids = self.rows = self.count = None
+        self._room = self._room_of = None       # the rows form's buffers and the stream that they were made on
+        self._captured = {}                     # those that captured calls write
         _settled(table.device)
 
     def lookup(self, ids, out, low=None, stream=None):
@@ -120,21 +122,34 @@ class ItemEmbedding:
         return H.embedding_fwd(self.table, ids, self.scale, out=out, low=low, stream=stream)
 
     def backward(self, dx, ids, stream=None):
-        """Takes the gradient of lookup's out.  In the rows form the buffers of an earlier batch of
-        this size are written again."""
+        """Takes the gradient of lookup's out.  In the rows form the buffers of an earlier batch are
+        written again (their entries past count hold nothing)."""
         if self.grad is not None:
             H.embedding_bwd(dx, ids, self.grad, self.scale, stream=stream)
             return
-        V, dim = self.table.shape
+        V = self.table.shape[0]
         cap = min(ids.shape[0], V)
-        if self.rows is None or self.rows.shape[0] != cap:
-            dev = self.table.device
-            # cleared on the stream that writes them: a fill queued on another could come after
-            with torch.cuda.stream(stream):
-                self.row_ids = torch.zeros(cap, dtype=torch.int64, device=dev)
-                self.rows = torch.zeros(cap, dim, dtype=torch.float32, device=dev)
-                self.count = torch.zeros(1, dtype=torch.int64, device=dev)
+        self._make_room(cap, stream)
+        row_ids, rows, self.count = self._room
+        self.row_ids, self.rows = row_ids[:cap], rows[:cap]
         H.embedding_bwd_rows(dx, ids, V, self.row_ids, self.rows, self.count, self.scale, stream=stream)
+
+    def _make_room(self, cap, stream):
+        """Buffers for cap rows, on the stream that writes them.  Those that a batch needs more than are
+        let go only once the streams that used them are through; those of a captured call stay."""
+        dev = self.table.device
+        on = None
+        if dev.type == "cuda":
+            on = torch.cuda.current_stream(dev) if stream is None else stream
+        if self._room is None or self._room[0].shape[0] < cap:
+            new = lambda *shape, t=torch.int64: H._empty(shape, t, dev, stream)
+            self._room = (new(cap), new(cap, self.table.shape[1], t=torch.float32), new(1))
+            self._room_of = on
+        elif on != self._room_of:
+            for t in self._room:
+                t.record_stream(on)
+        if on is not None and torch.cuda.is_current_stream_capturing():
+            self._captured[id(self._room)] = self._room
 
     def zero_grad(self, stream=None):
         """Clears the dense gradient, on the stream that the next backward runs on."""

@@ -128,3 +128,31 @@ def test_gradients_are_cleared_on_the_given_stream(monkeypatch):
         clear(stream="side")
         assert set(fills) == {"side"} and all(not bool(t.any()) for t in filled)
         clear()
+
+
+def test_rows_gradient_buffers_grow_and_are_not_cleared(monkeypatch):
+    """Batches of changing size share the buffers of the largest so far; what the gradient does not write is not touched."""
+    wrote = []
+
+    def rows_gradient(dx, ids, V, row_ids, rows, count, scale, stream=None):
+        assert row_ids.shape == (min(ids.shape[0], V),) and rows.shape == (row_ids.shape[0], 8) and rows.is_contiguous()
+        wrote.append((row_ids.data_ptr(), rows.data_ptr(), count.data_ptr()))
+        count.fill_(1)
+        row_ids[:1] = 7
+        rows[:1] = 2.0
+    monkeypatch.setattr(H, "embedding_bwd_rows", rows_gradient)
+    emb = S.ItemEmbedding(torch.zeros(90, 8), rows=True)
+    run = lambda T: emb.backward(torch.zeros(T, 8), torch.zeros(T, dtype=torch.int64))
+    run(50)
+    emb.rows.fill_(9.0)
+    emb.row_ids.fill_(3)
+    for T in (20, 50, 1, 49):
+        run(T)
+        assert emb.rows.shape == (T, 8) and bool((emb.rows[1:] == 9).all()) and bool((emb.row_ids[1:] == 3).all())
+    assert len(set(wrote)) == 1
+    run(70)
+    assert emb.rows.shape == (70, 8) and len(set(wrote)) == 2
+    run(500)                             # no more rows than items
+    assert emb.rows.shape == (90, 8)
+    run(0)
+    assert emb.rows.shape == (0, 8)

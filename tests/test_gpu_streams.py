@@ -146,3 +146,54 @@ def test_first_run_on_a_side_stream_behind_a_busy_current_one(kind):
         dx = step.run(stream=side)
         torch.cuda.synchronize()
         same(parts(kind, step, dx), want, "bf16")
+
+
+def rows_of(emb):
+    n = int(emb.count)
+    return emb.row_ids[:n].clone(), emb.rows[:n].clone()
+
+
+def test_rows_gradient_after_a_change_of_stream_and_size():
+    """Buffers made on one stream, written on another that is behind, and replaced by larger ones: their memory goes to nobody
+    while they are written.  Sums of ones are exact."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    busy = torch.ones(64 << 20, device="cuda")
+    emb = S.ItemEmbedding(torch.zeros(5000, 64, device="cuda"), scale=1.0, rows=True)
+    small, large = torch.arange(2000, device="cuda"), torch.arange(4000, device="cuda").repeat(2)
+    one = torch.ones(8000, 64, device="cuda")
+    torch.cuda.synchronize()
+    emb.backward(one[:2000], small, stream=a)
+    a.synchronize()
+    with torch.cuda.stream(b):
+        for _ in range(50):
+            busy.mul_(1.0)
+    emb.backward(one[:2000], small, stream=b)
+    emb.backward(one, large, stream=b)
+    with torch.cuda.stream(a):
+        fresh = [torch.full((2000, 64), 7.0, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(bool((f == 7.0).all()) for f in fresh)
+    ids, rows = rows_of(emb)
+    assert torch.equal(ids, torch.arange(4000, device="cuda")) and bool((rows == 2.0).all())
+
+
+def test_captured_rows_gradient_after_a_larger_batch():
+    """A captured gradient's buffers stay when a later batch needs larger ones."""
+    emb = S.ItemEmbedding(torch.zeros(5000, 64, device="cuda"), scale=1.0, rows=True)
+    small, large = torch.arange(2000, device="cuda"), torch.arange(4000, device="cuda").repeat(2)
+    one = torch.ones(8000, 64, device="cuda")
+    emb.backward(one[:2000], small)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        emb.backward(one[:2000], small)
+    at, where = emb.rows.data_ptr(), emb.rows.shape
+    emb.backward(one, large)
+    assert emb.rows.data_ptr() != at
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    fresh = [torch.full(where, 7.0, device="cuda") for _ in range(4)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(bool((f == 7.0).all()) and f.data_ptr() != at for f in fresh)
+    ids, rows = rows_of(emb)
+    assert ids.numel() == 4000 and bool((rows == 2.0).all())
