@@ -636,25 +636,34 @@ __global__ void __launch_bounds__(kThreads<TPR>, bwd_resident(kThreads<TPR>)) bl
 }
 
 // grads.p[i][c] += sum over the CTAs of partial[cta][i][c], in the order of
-// the CTAs within each of 32 strips, then of the strips.
+// the CTAs within each of 32 strips, then of the strips.  Parameters that share
+// a gradient (two norms with one gamma) are added one after another by the
+// CTAs of the first.
 constexpr int kStrips = 32;
 __global__ void __launch_bounds__(32 * kStrips) block_norm_join_kernel(const float* __restrict__ partial, int ctas,
                                                                        int d, GradPtrs grads) {
   __shared__ float strip[kStrips][32];
-  float* const out = grads.p[blockIdx.y];
+  const int first = blockIdx.y;
+  float* const out = grads.p[first];
   if (!out) return;
+  for (int i = 0; i < first; ++i)
+    if (grads.p[i] == out) return;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
-  const float* src = partial + (int64_t)blockIdx.y * d + c;
-  float t = 0.f;
-  if (c < d)
+  for (int i = first; i < kParams; ++i) {
+    if (grads.p[i] != out) continue;
+    const float* src = partial + (int64_t)i * d + c;
+    float t = 0.f;
+    if (c < d)
 #pragma unroll 4
-    for (int i = w; i < ctas; i += kStrips) t += src[(int64_t)i * kParams * d];
-  strip[w][lane] = t;
-  __syncthreads();
-  if (w == 0 && c < d) {
+      for (int k = w; k < ctas; k += kStrips) t += src[(int64_t)k * kParams * d];
+    strip[w][lane] = t;
+    __syncthreads();
+    if (w == 0 && c < d) {
 #pragma unroll
-    for (int k = 1; k < kStrips; ++k) t += strip[k][lane];
-    out[c] += t;
+      for (int k = 1; k < kStrips; ++k) t += strip[k][lane];
+      out[c] += t;
+    }
+    __syncthreads();
   }
 }
 
@@ -860,6 +869,12 @@ hstu_status hstu_block_norm_bwd(const hstu_config* cfg, const hstu_block_norm* b
       HSTU_TRY(meta(all[i], all[i] ? 1 : 0, 4));
       g.p[i] = kind[i] != HSTU_NORM_NONE ? all[i] : nullptr;
       any = any || g.p[i];
+      // the same array, or apart
+      for (int k = 0; k < i; ++k) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(all[i]), b = reinterpret_cast<uintptr_t>(all[k]);
+        if (all[i] && all[k] && a != b && (a < b ? b - a : a - b) < (size_t)cfg->d_model * sizeof(float))
+          return HSTU_ERR_INVALID;
+      }
     }
   }
   if (T == 0) return HSTU_OK;

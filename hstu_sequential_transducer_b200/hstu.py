@@ -627,7 +627,8 @@ class BlockNorm:
 
 @dataclass
 class BlockNormGrads:
-    """fp32 [d] gradients of a BlockNorm's parameters, accumulated; None: not wanted."""
+    """fp32 [d] gradients of a BlockNorm's parameters, accumulated; None: not wanted.  Parameters that
+    are one tensor may have one gradient, which takes the sum."""
     post_gamma: Optional[torch.Tensor] = None
     post_beta: Optional[torch.Tensor] = None
     res_scale: Optional[torch.Tensor] = None

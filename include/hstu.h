@@ -501,7 +501,8 @@ typedef struct {
 } hstu_block_norm;
 
 /* Gradients of the members above, fp32 [d], accumulated (+=); NULL is skipped,
- * and so are those of a norm that is not there (HSTU_NORM_NONE). */
+ * and so are those of a norm that is not there (HSTU_NORM_NONE).  Members may
+ * be one array (parameters that two norms share), but not overlap otherwise. */
 typedef struct {
   float* post_gamma;
   float* post_beta;

@@ -147,3 +147,15 @@ def test_joint_without_block_output():
     for kw in ({"gate": torch.zeros(4, 64, dtype=torch.bfloat16)}, {"y": torch.zeros(4, 64)}):
         with pytest.raises(ValueError, match="need b"):
             H.block_norm_fwd(cfg(), H.BlockNorm(), x, **kw)
+
+
+def test_parameter_gradients_may_be_one_array_but_not_overlap(L):
+    """Refused before any launch; the same array twice passes the checks as far as the workspace's."""
+    c = cfg()
+    bn = H.CBlockNorm(post_kind=1, pre_kind=2, gate_act=0)
+    call = lambda **g: L.hstu_block_norm_bwd(ctypes.byref(c), ctypes.byref(bn), P1, P2, None, 0, P1, P2, P3, 4, P4, None, None, 0,
+                                             ctypes.byref(H.CBlockNormGrads(**g)), WS, 0, None)
+    assert call(post_gamma=P1, pre_gamma=P1 + 4) == INVALID
+    assert call(pre_beta=P1, res_scale=P1 + 252) == INVALID
+    assert call(post_gamma=P1, pre_gamma=P1) == WORKSPACE
+    assert call(post_gamma=P1, pre_gamma=P1 + 256) == WORKSPACE

@@ -274,3 +274,23 @@ def test_other_stream_and_graph():
     H.block_norm_bwd(cfg, bn, y, b, u, stats, dy=dy, dh=dh, dx=dx, grads=g)
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(dx, dx2) and torch.equal(g.post_gamma, g2.post_gamma)
+
+
+@pytest.mark.parametrize("T", [1, 2, 300, 20_000])
+@pytest.mark.parametrize("shared", [("post_gamma", "pre_gamma"), ("post_beta", "pre_beta", "res_scale"), PARAMS])
+def test_parameters_that_share_a_gradient(T, shared):
+    """One array for several parameters takes the sum of theirs, added in their order onto what it held: the separate gradients
+    give it to within the len(shared) fp32 additions of values no larger than the magnitudes added."""
+    d = 224
+    cfg, bn, p, x, b, u, rnd = make(T, d, "bf16", "f32", "layer", "layer", "silu", ALL)
+    stats = torch.empty(T, 4, device=DEV)
+    y, _ = H.block_norm_fwd(cfg, bn, x, b, u, stats=stats)
+    dy, dh = rnd(T, d), rnd(T, d)
+    apart = H.BlockNormGrads.zeros_like(bn)
+    H.block_norm_bwd(cfg, bn, y, b, u, stats, dy=dy, dh=dh, grads=apart)
+    prior = rnd(d)
+    for _ in range(2):
+        one = prior.clone()
+        H.block_norm_bwd(cfg, bn, y, b, u, stats, dy=dy, dh=dh, grads=H.BlockNormGrads(**{n: one for n in shared}))
+        terms = np.stack([f64(prior)] + [f64(getattr(apart, n)) for n in shared])
+        assert np.all(np.abs(f64(one) - terms.sum(0)) <= len(shared) * U * np.abs(terms).sum(0))
