@@ -377,13 +377,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(PairSource s
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    uint32_t at = 0xffffffffu;          // the next pass's counter of the pair
-    if (in[i]) {
-      const uint32_t to = count[warp][digit[i]] + rank[i];
-      out[to] = pair[i];
-      at = to / kTile * kDigits + next.digit(pair[i].x);
-    }
+    const uint32_t to = in[i] ? count[warp][digit[i]] + rank[i] : 0u;
+    if (in[i]) out[to] = pair[i];
     if (next_hist) {
+      // the next pass's counter of the pair (after the last one there is none, nor a digit: its shift may be 32)
+      const uint32_t at = in[i] ? to / kTile * kDigits + next.digit(pair[i].x) : 0xffffffffu;
       // once for those of the pair's peers that share the first one's counter (a popular item's all do)
       const int first = __ffs(peers[i]) - 1;
       const uint32_t lead = __shfl_sync(0xffffffffu, at, first < 0 ? 0 : first);

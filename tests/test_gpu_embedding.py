@@ -247,3 +247,45 @@ def test_other_stream_and_graph(T):
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(bufs[0][2], want[1])
+
+
+@pytest.mark.parametrize("V", [300, 300_000, 20_000_000, (1 << 28) + 9, (1 << 31) - 1])
+@pytest.mark.parametrize("T", [40_001, 400_001])
+def test_rows_gradient_of_every_pass_count(T, V):
+    """The sort by launches, its tiles' counts added up by each tile or scanned (up to 96 tiles, above): one to four digits, ids over
+    the whole catalogue, many of them neighbours of the borders of a digit; the same bits from a second call."""
+    rng = np.random.default_rng(V)
+    ids = rng.integers(0, V, size=T)
+    near = rng.integers(0, 4, size=T) * (V // 4) + rng.integers(-3, 4, size=T)
+    some = rng.random(T) < 0.3
+    ids[some] = near[some]                                   # popular items, among them -1 .. -3 and V .. V + 2 as padding
+    dim = 3
+    dout = rows_of(rng, T, dim, torch.float32)
+    cap = min(T, V)
+    new = lambda: (torch.full((cap,), -7, dtype=torch.int64, device=DEV), torch.full((cap, dim), 5.0, device=DEV),
+                   torch.full((1,), -7, dtype=torch.int64, device=DEV))
+    dev_ids = torch.from_numpy(ids).to(DEV)
+    row_ids, rows, count = H.embedding_bwd_rows(dout, dev_ids, V, *new())
+    real = (ids >= 0) & (ids < V)
+    uniq, inv = np.unique(ids[real], return_inverse=True)
+    n = len(uniq)
+    assert int(count.item()) == n
+    np.testing.assert_array_equal(row_ids.cpu().numpy()[:n], uniq)
+    assert bool((row_ids[n:] == -7).all()) and bool((rows[n:] == 5).all())
+    local = np.full(T, -1)
+    local[real] = inv
+    check_grad(dout, local, n, dim, 1.0, np.zeros((n, dim)), f64(rows)[:n])
+    again = H.embedding_bwd_rows(dout, dev_ids, V, *new())
+    assert torch.equal(again[0], row_ids) and torch.equal(again[1], rows) and int(again[2]) == n
+
+
+@pytest.mark.parametrize("T", [40_001, 400_001])
+def test_dense_gradient_of_three_digits(T):
+    rng = np.random.default_rng(T)
+    V, dim = 300_000, 3
+    ids = rng.integers(-5, V + 5, size=T)
+    dout = rows_of(rng, T, dim, torch.bfloat16)
+    prior = torch.from_numpy(rng.standard_normal((V, dim)).astype(np.float32)).to(DEV)
+    g = H.embedding_bwd(dout, torch.from_numpy(ids).to(DEV), prior.clone(), 1.5)
+    check_grad(dout, ids, V, dim, 1.5, f64(prior), f64(g))
+    assert torch.equal(g, H.embedding_bwd(dout, torch.from_numpy(ids).to(DEV), prior.clone(), 1.5))
