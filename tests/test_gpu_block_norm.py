@@ -294,3 +294,82 @@ def test_parameters_that_share_a_gradient(T, shared):
         H.block_norm_bwd(cfg, bn, y, b, u, stats, dy=dy, dh=dh, grads=H.BlockNormGrads(**{n: one for n in shared}))
         terms = np.stack([f64(prior)] + [f64(getattr(apart, n)) for n in shared])
         assert np.all(np.abs(f64(one) - terms.sum(0)) <= len(shared) * U * np.abs(terms).sum(0))
+
+
+# A CTA's loop over its rows: rows are copied ahead into slots that the step before leaves, parameters' sums go on from step to
+# step.  A team of threads takes 4 rows at a time forward, 1 or 2 backward.
+def team_of(d):
+    if d > 256:
+        return (d + 255) // 256 * 32
+    t = 4
+    while 8 * t < d:
+        t *= 2
+    return t
+
+
+def rows_a_step(d, backward=False):
+    """Rows that the resident CTAs take together in one step."""
+    team = team_of(d)
+    threads = max(team, 128) if team < 96 else team
+    if not backward:
+        rows, resident = 4, 2 if threads > 192 else 384 // threads
+    else:
+        rows = 1 if team == 96 or 128 < team < 256 else 2
+        resident = (512 if rows == 1 else 256) // threads
+    return threads // team * rows * resident * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def three_steps(d):
+    """Rows for two steps of every CTA forward, a third of some and a last one in part; more steps backward."""
+    assert rows_a_step(d, True) <= rows_a_step(d)
+    return 2 * rows_a_step(d) + rows_a_step(d) // 3 + 5
+
+
+TYPES = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
+
+
+@pytest.mark.parametrize("d", [32, 224, 512, 768, 1024, 1056, 1536, 1792, 2048])
+@pytest.mark.parametrize("kind", range(3))
+def test_many_steps(d, kind):
+    """Every kind of team (below a warp, whole warps, one or two rows backward), each with three types and kinds of norm and gate."""
+    dt, io = TYPES[(kind + d // 32) % 3]
+    post, pre, gate = [("layer", "layer", "silu"), (None, "rms", "sigmoid"), ("rms", None, "absent")][kind]
+    T = three_steps(d)
+    cfg, bn, p, x, b, u, rnd = make(T, d, dt, io, post, pre, gate, ALL, seed=d + kind)
+    y, h, st, c, q = forward_and_check(cfg, bn, p, x, b, u, T, d)
+    backward_and_check(cfg, bn, p, y, b, u, st, rnd, T, d, c, q)
+
+
+@pytest.mark.parametrize("d", [32, 512, 768, 2048])
+@pytest.mark.parametrize("pre", ["layer", None])
+def test_many_steps_at_the_start_of_a_stack(d, pre):
+    """Without a block: x alone is copied ahead."""
+    T = three_steps(d)
+    cfg, bn, p, x, _, _, rnd = make(T, d, "bf16", "f32", "layer", pre, "absent", ALL, seed=d)
+    y, h, st, c, q = forward_and_check(cfg, bn, p, x, None, None, T, d)
+    backward_and_check(cfg, bn, p, y, None, None, st, rnd, T, d, c, q)
+
+
+@pytest.mark.parametrize("d", [64, 512, 1056, 2048])
+@pytest.mark.parametrize("post", ["layer", None])
+def test_many_steps_in_place(d, post):
+    """y over x, and no h: the rows copied ahead are others than those that are written."""
+    T = three_steps(d)
+    cfg, bn, p, x, b, u, rnd = make(T, d, "bf16", "f32", post, "rms", "silu", ALL, seed=d)
+    y, h = H.block_norm_fwd(cfg, bn, x, b, u)
+    again = x.clone()
+    y2, h2 = H.block_norm_fwd(cfg, bn, again, b, u, y=again)
+    assert y2 is again and torch.equal(y2, y) and torch.equal(h2, h)
+    y3, h3 = H.block_norm_fwd(cfg, bn, x, b, u, want_h=False)
+    assert h3 is None and torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("T", [2, 3, 4, 8])
+@pytest.mark.parametrize("d", [512, 768, 1024, 1056, 2048])
+def test_two_steps_by_one_cta(T, d):
+    """Two steps backward are left to one CTA, which adds its sums to the gradients itself (2 rows at 768 and
+    1,056, which take one a step; 3 and 4 at 1,024 and 2,048; 8 at 512, two teams)."""
+    for dt, io in TYPES:
+        cfg, bn, p, x, b, u, rnd = make(T, d, dt, io, "layer", "rms", "silu", ALL, seed=T)
+        y, h, st, c, q = forward_and_check(cfg, bn, p, x, b, u, T, d)
+        backward_and_check(cfg, bn, p, y, b, u, st, rnd, T, d, c, q)
