@@ -20,6 +20,7 @@ on CPU in the tests.
 """
 from __future__ import annotations
 
+import warnings
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -90,9 +91,22 @@ def layer_buckets(flat: torch.Tensor, sizes: Sequence[int]) -> List[torch.Tensor
 
 
 def default_group_bucketing(step) -> Optional[BucketedAllReduce]:
-    """Bucketed all-reduce of a TrainStep's gradients over the default process
-    group, or None when running alone."""
+    """Bucketed all-reduce of a TrainStep's layer gradients over the default
+    process group, or None when running alone.
+
+    The buckets are the layers'.  An item embedding's gradient is not among
+    them: it is final only at the end of the run, and as rows it has other
+    items on every rank.  The caller sums it (a dense one: all_reduce of
+    step.embedding.grad after the run); a step with an embedding is warned
+    about that here.  A step without one flat gradient buffer
+    (NormedTrainStep) is refused."""
     import torch.distributed as dist
     if not (dist.is_available() and dist.is_initialized()) or dist.get_world_size() == 1:
         return None
+    if not hasattr(step, "flat_grads"):
+        raise TypeError(f"{type(step).__name__} has no per-layer gradient buckets: all-reduce its "
+                        "gradients after the run")
+    if getattr(step, "embedding", None) is not None:
+        warnings.warn("the item embedding's gradient is not in the layers' buckets: sum it over the "
+                      "ranks after the run", stacklevel=2)
     return BucketedAllReduce(layer_buckets(step.flat_grads, step.layer_grad_sizes), dist)

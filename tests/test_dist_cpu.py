@@ -184,3 +184,29 @@ def test_lpt_split_small_cases():
     assert dp.lpt_shards([4], 3) == [[0], [], []]
     with pytest.raises(ValueError):
         dp.lpt_shards([1], 0)
+
+
+def test_gradients_outside_the_layers_buckets_are_not_left_out_silently(monkeypatch):
+    """A step with an item embedding: the buckets are the layers', and the caller is told that the table's gradient is not in
+    them.  A stack with norms has no buckets and is refused by name.  Alone, nothing is asked for."""
+    import warnings
+    from hstu_sequential_transducer_b200 import build, dp
+    from hstu_sequential_transducer_b200 import hstu as H
+    from hstu_sequential_transducer_b200 import stack as S
+    from hstu_sequential_transducer_b200 import workloads as W
+    build.build()
+    w = W.custom([9, 4], d=64, H=2, dtype="bf16", N=16.0, backward=True, layers=2)
+    dw = S.DeviceWorkload.from_workload(w, device="cpu")
+    plain = S.TrainStep(dw)
+    embedded = S.TrainStep(dw, embedding=S.ItemEmbedding(torch.zeros(5, 64)), ids=torch.zeros(dw.T, dtype=torch.int64))
+    normed = S.NormedTrainStep(dw, [H.BlockNorm() for _ in range(3)])
+    assert all(dp.default_group_bucketing(s) is None for s in (plain, embedded, normed))
+    monkeypatch.setattr(dist, "is_initialized", lambda: True)
+    monkeypatch.setattr(dist, "get_world_size", lambda: 2)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        assert len(dp.default_group_bucketing(plain).buckets) == 2
+    with pytest.warns(UserWarning, match="embedding"):
+        assert len(dp.default_group_bucketing(embedded).buckets) == 2
+    with pytest.raises(TypeError, match="NormedTrainStep"):
+        dp.default_group_bucketing(normed)
