@@ -315,6 +315,8 @@ class NormedTrainStep:
             raise ValueError(f"a stack of {L} layers has {L + 1} joints, got {len(joints)}")
         self.dw, self.joints = dw, joints
         self.gates = [None] * L if gates is None else list(gates)
+        if len(self.gates) != L:
+            raise ValueError(f"a stack of {L} layers has a gate or None for each, got {len(self.gates)}")
         dt = H.torch_dtype(cfg.dtype)
         d = cfg.d_model
         self.store = SavedBlocks(dw, checkpoints)
@@ -345,6 +347,9 @@ class NormedTrainStep:
         """Forward, then backward from dy; returns dX (a buffer of this step)."""
         dw, cfg, st = self.dw, self.dw.cfg, {"stream": stream}
         L = len(dw.layers)
+        g = dw.dy if dy is None else dy
+        if g is None:
+            raise ValueError("the workload has no dy: run needs one")
         H.block_norm_fwd(cfg, self.joints[0], self.y_[0], h=self.h[0] if L else None, stats=self.stats[0],
                          want_h=L > 0, **st)
         for i, w in enumerate(dw.layers):
@@ -358,7 +363,6 @@ class NormedTrainStep:
             last = i + 1 == L
             H.block_norm_fwd(cfg, self.joints[i + 1], self.y_[i], self.b[i], self.gates[i], y=self.y_[i + 1],
                              h=None if last else self.h[i + 1], stats=self.stats[i + 1], want_h=not last, **st)
-        g = dw.dy if dy is None else dy
         dh = None
         for i in range(L - 1, -1, -1):
             w, gr, v = dw.layers[i], self.grads[i], self.views[i]

@@ -156,3 +156,18 @@ def test_rows_gradient_buffers_grow_and_are_not_cleared(monkeypatch):
     assert emb.rows.shape == (90, 8)
     run(0)
     assert emb.rows.shape == (0, 8)
+
+
+def test_normed_steps_refuse_missing_gates_and_a_missing_gradient(lib):
+    """A gate (or None) for each layer, no fewer and no more; a run without an upstream gradient would give zeros for all."""
+    w = W.custom([9, 4], d=64, H=2, dtype="bf16", N=16.0, layers=2)
+    dw = S.DeviceWorkload.from_workload(w, device="cpu")
+    joints, gate = [H.BlockNorm() for _ in range(3)], torch.zeros(dw.T, 64, dtype=torch.bfloat16)
+    for gates in ([gate], [gate] * 3, []):
+        with pytest.raises(ValueError, match="gate"):
+            S.NormedTrainStep(dw, joints, gates)
+    step = S.NormedTrainStep(dw, joints, [gate, None])
+    assert dw.dy is None
+    with pytest.raises(ValueError, match="dy"):
+        step.run()
+    assert not lib.calls
