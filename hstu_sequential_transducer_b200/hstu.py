@@ -168,9 +168,14 @@ def ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle: torch.cuda.current_stream() makes a Stream object
+# of it at every call, which takes as long as the launch itself.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def stream_ptr(stream: Optional[torch.cuda.Stream] = None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def torch_dtype(dtype: int):
@@ -478,12 +483,6 @@ def _flat(where, name, t, shape, dtype, device):
         return t.data_ptr()
     raise ValueError(f"{where}: {name} must be contiguous {tuple(shape)} {dtype} on {device}, got "
                      f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
-
-
-# The current stream's handle: torch.cuda.current_stream() makes a Stream object
-# of it at every call, which takes as long as the launch itself.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _launch(where, device, stream, f, *args, ws_bytes=None):
