@@ -11,7 +11,7 @@
 //   dgamma2 += sum dh n2, dbeta2 += sum dh       (no mean(.) term for RMS)
 //
 // Memory-bound (a token reads 10d bytes and writes 6d in the forward, reads
-// 16d and writes 8d in the backward, with bf16 operands and an fp32 residual
+// 18d and writes 8d in the backward, with bf16 operands and an fp32 residual
 // stream).  A team of TPR threads, 8 columns a thread (a power of two below a
 // warp, else whole warps), takes R rows at a time: 4 in the forward, 1 or 2 in
 // the backward.  The columns stay the same, so the parameters are read once and
@@ -26,7 +26,9 @@
 // Measured at 131,072 x 1,024, bf16 operands, fp32 residual stream: forward
 // 340-343 us (6.3 TB/s; 372 with 4 resident CTAs, which takes registers from
 // each), backward 547 us (6.4 TB/s; 599 with 3 CTAs; 566 with one row at a time and 4).
-// With a bf16 residual stream (half the bytes, the same instructions) 0.7 of the copy rate.
+// With a bf16 residual stream 0.7 of the copy rate: half the bytes, but the same joins by
+// the same 12 (forward) and 8 (backward) warps on a multiprocessor, which fill neither
+// DRAM (45 and 54 %, at 32,768 x 1,024) nor the issue slots (54 and 50 %).
 #include "args.h"
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -550,7 +552,8 @@ __global__ void __launch_bounds__(kThreads<TPR>, bwd_resident(kThreads<TPR>)) bl
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (full || r0 + i < p.rows) cols.store(dx + (r0 + i) * d, e[i]);
-    // a part's slots are free once its values have gone into a sum or a store
+    // a part's slots are free once its values have been taken: a thread's loads come before
+    // the copies that it starts after them
     fetch_e(base + step);
     copy_wait<1>();                    // b and u are here
     if (b) {

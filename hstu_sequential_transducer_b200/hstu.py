@@ -648,8 +648,8 @@ class BlockNormGrads:
 def block_norm_fwd(cfg, bn: BlockNorm, x, b=None, gate=None, y=None, h=None, stats=None, want_h=True,
                    stream=None):
     """y = x + res_scale * (Norm_post(b) * act(gate)), h = Norm_pre(y); returns (y, h).  Without b
-    (the start of a stack) y is x; with want_h False (its end) h is None.  stats: fp32 [T][4], kept
-    for block_norm_bwd."""
+    (the start of a stack) y is x; with want_h False (its end) h is None, and the backward has no dh.
+    stats: fp32 [T][4], kept for block_norm_bwd."""
     where = "block_norm_fwd"
     dev, d, T = x.device, cfg.d_model, x.shape[0]
     io, dt = torch_dtype(cfg.io_dtype), torch_dtype(cfg.dtype)

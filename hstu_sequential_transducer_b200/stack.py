@@ -306,7 +306,8 @@ class NormedTrainStep:
     with Norm_pre of joint i before block i, and Norm_post, s and the gate's activation of joint
     i + 1 after it (so joints has one more entry than the stack has layers, the first joint's
     Norm_post and the last one's Norm_pre are not used).  gates: a [T][d] tensor (cfg->dtype) or
-    None for each block; their gradients are left in dgates.  checkpoints as in TrainStep."""
+    None for each block; their gradients are left in dgates.  checkpoints: the saved blocks as in
+    TrainStep; the joints' y and b (8d bytes a token and layer with an fp32 residual stream) are kept."""
 
     def __init__(self, dw: DeviceWorkload, joints: List[H.BlockNorm], gates=None,
                  checkpoints: Optional[str] = None):

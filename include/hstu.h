@@ -482,7 +482,9 @@ hstu_status hstu_embedding_bwd_rows(const void* dout, int32_t dout_dtype, int64_
  * what hstu_proj_in_bwd writes and db the dY of hstu_proj_out_bwd.  u and du
  * may be columns of wider rows (gate_stride, dgate_stride in elements, at
  * least d and a multiple of 16 bytes); all else is contiguous.  stats fp32
- * [T][4] holds each row's m and r after the block, then before the next one.
+ * [T][4] holds each row's m and r after the block, then before the next one; 0
+ * and 1 for a norm that is not there or, h being NULL, not taken (there is no dh
+ * for such a forward).
  * Without a block (b NULL) y = x, is not written, and u, s and Norm_post do
  * not apply. */
 typedef enum { HSTU_NORM_NONE = 0, HSTU_NORM_LAYER = 1, HSTU_NORM_RMS = 2 } hstu_norm_kind;
