@@ -263,7 +263,8 @@ class TrainStep:
         """Forward (keeping activations) then backward from dy; returns dX.
         on_layer_grads(i), when given, is called right after layer i's
         backward has been issued (layers in reverse order), e.g. to start the
-        all-reduce of that layer's gradients."""
+        all-reduce of that layer's gradients, with the run's stream as the
+        current one."""
         dw = self.dw
         L = len(dw.layers)
         ch = self.chain
@@ -285,7 +286,8 @@ class TrainStep:
                   dy_low=self.dlow[(i + 1) % 2] if ch and i < L - 1 else None,
                   dx_low=self.dlow[i % 2] if ch and i > 0 else None)
             if on_layer_grads is not None:
-                on_layer_grads(i)
+                with torch.cuda.stream(stream):
+                    on_layer_grads(i)
             g = out
         if emb is not None:
             emb.backward(g, self.ids, stream=stream)

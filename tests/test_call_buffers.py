@@ -171,3 +171,25 @@ def test_normed_steps_refuse_missing_gates_and_a_missing_gradient(lib):
     with pytest.raises(ValueError, match="dy"):
         step.run()
     assert not lib.calls
+
+
+def test_layer_gradients_are_handed_over_on_the_stream_of_the_run(lib, monkeypatch):
+    """on_layer_grads starts collectives, which are ordered after the current stream: that of the run."""
+    w = W.custom([9, 4], d=64, H=2, dtype="bf16", N=16.0, backward=True, layers=3)
+    step = S.TrainStep(S.DeviceWorkload.from_workload(w, device="cpu"))
+    side, current = types.SimpleNamespace(cuda_stream=11), [None]
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    seen = []
+    for stream in (side, None):
+        step.run(stream=stream, on_layer_grads=lambda i: seen.append((i, current[-1])))
+    assert seen == [(i, s) for s in (side, None) for i in (2, 1, 0)]
