@@ -464,9 +464,11 @@ class StochasticLength:
         self.gather_index = torch.empty(max(dw.T, 1), dtype=torch.int64, device=dev)
         self.x = torch.empty_like(dw.x)
         self.timestamps = torch.empty_like(dw.timestamps)
+        self._stream = None                     # of the last run
 
     def run(self, keep_draw: torch.Tensor, keys: torch.Tensor, stream=None):
         dw = self.dw
+        self._stream = torch.cuda.current_stream(dw.x.device) if stream is None else stream
         H.stochastic_length(dw.offsets, dw.num_targets, self.sub_len, keep_draw, keys,
                             self.new_offsets, self.gather_index, stream=stream)
         count = self.new_offsets[dw.B:]
@@ -475,6 +477,7 @@ class StochasticLength:
 
     def batch(self) -> DeviceWorkload:
         dw = self.dw
-        t = int(self.new_offsets[dw.B].item())
+        with torch.cuda.stream(self._stream):   # comes after the run
+            t = int(self.new_offsets[dw.B].item())
         return DeviceWorkload(dw.cfg, self.x[:t], self.new_offsets, self.timestamps[:t],
                               dw.num_targets, dw.layers, None, dw.w)

@@ -197,3 +197,28 @@ def test_captured_rows_gradient_after_a_larger_batch():
     assert all(bool((f == 7.0).all()) and f.data_ptr() != at for f in fresh)
     ids, rows = rows_of(emb)
     assert ids.numel() == 4000 and bool((rows == 2.0).all())
+
+
+def test_sampled_batch_of_a_run_on_another_stream():
+    """batch() right after a run on a stream that is behind: it waits for that run, whatever stream is the current one."""
+    w = W.custom([170] * 3, d=128, H=2, dtype="bf16", N=400.0, layers=1, mean_gap=900.0, seed=5)
+    dw = S.DeviceWorkload.from_workload(w)
+    sl = S.StochasticLength(dw, 1.2)
+    assert sl.sub_len < 170
+    none, all_ = torch.full((3,), -1, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    keys = torch.arange(dw.T, dtype=torch.int32, device="cuda")
+    want = []
+    for draw in (none, all_):
+        sl.run(draw, keys)
+        b = sl.batch()
+        want.append((b.T, b.x.clone(), b.timestamps.clone()))
+    assert want[0][0] != want[1][0]
+    side, busy = torch.cuda.Stream(), torch.ones(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    for draw, (t, x, ts) in list(zip((none, all_), want)) * 2:
+        with torch.cuda.stream(side):
+            for _ in range(50):
+                busy.mul_(1.0)
+        sl.run(draw, keys, stream=side)
+        b = sl.batch()
+        assert b.T == t and torch.equal(b.x, x) and torch.equal(b.timestamps, ts)
